@@ -364,6 +364,161 @@ KVQ_API kvq_status kvq_decode_step_host(const kvq_cache* cache, const void* q_ho
                                         int32_t keep_groups, float softmax_scale, float* out_host,
                                         void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * ------------------------------------------------------------------ paged cache
+ *
+ * The same low-bit keys and values kept in pages of a pool, for servers whose
+ * requests come and go: requests hold page lists (block tables) instead of
+ * `capacity` tokens each, a scheduling step builds its block tables and slot
+ * map on the device (kvq_page_plan), new tokens are quantized into the slots
+ * they got (kvq_paged_append), a decode step follows the block tables
+ * (kvq_paged_decode), and cached tokens can be read back as dense rows
+ * (kvq_paged_gather), e.g. for prompt attention over a cached prefix.
+ * No call synchronizes the host or needs a length on it, so a whole step can
+ * be captured into a graph and replayed.
+ *
+ * A page holds page_tokens consecutive token positions of one request for
+ * every kv head.  slot = page * page_tokens + position % page_tokens.
+ *
+ * Pool layout: [num_pages][kv_heads][page_tokens / 64][block], a block holding
+ * 64 tokens of one head, its parts one after another:
+ *  k codes   [32 channel groups p][64 tokens]: 2 bytes (INT4) or 1 byte (INT2)
+ *            per token and group of 4 channels.  A row is 8 chunks of 8 tokens;
+ *            the chunk of tokens 8u .. 8u+7 sits at chunk position
+ *            u XOR 2 (p & 3) for INT4, u XOR 4 ((p >> 1) & 1) for INT2.  In an
+ *            INT4 chunk token 8u + 2i + e has channels 4p, 4p+1 (low, high
+ *            nibble) in byte 4i + e and channels 4p+2, 4p+3 in byte 4i + 2 + e;
+ *            in an INT2 chunk token 8u + r has byte r, channel 4p+j at bits 2j.
+ *  k scales  fp16 [i = 0..3][u = 0..7][e = 0, 1][4 groups], token 8u + 2i + e
+ *  k zeros   fp16 [i / 2][u][group / 2][i % 2][e][group % 2]
+ *  k ch0     bf16 [64], channel 0 of each key (keep_ch0 only)
+ *  v codes   [rows][64 bytes]: row r holds channels 2r, 2r+1 (INT4) or
+ *            4r .. 4r+3 (INT2), low bits first; token t's byte is byte
+ *            16 (t / 16) + 4 ((t % 8) / 2) + 2 ((t % 16) / 8) + t % 2 of each row
+ *  v scales, v zeros: as k scales
+ * Every byte belongs to one token, so appends of different tokens never share
+ * one.
+ *
+ * Supported: head_dim = 128, group_size = 32, prune_granule = 4, k_bits and
+ * v_bits in {2, 4}, page_tokens a multiple of 64 up to 4096, rotate_k 0 or 1,
+ * num_pages * page_tokens < 2^31; pages 128-byte aligned.
+ */
+typedef struct {
+  int32_t num_pages, page_tokens, kv_heads, head_dim;
+  int32_t k_bits, v_bits, group_size, prune_granule;
+  int32_t rotate_k;  /* 1: keys and queries pass through the orthonormal Walsh-Hadamard transform */
+  int32_t keep_ch0;  /* 1: rotated channel 0 of each key is kept in bf16, unquantized             */
+  int32_t rotate_v;  /* 1: values are rotated before quantization, decode outputs rotated back    */
+  float v_clip;      /* value clipping ratio in (0, 1], as in kvq_cache                           */
+  void* pages;       /* device memory of kvq_paged_bytes bytes, caller-owned                      */
+} kvq_paged_cache;
+
+/* Bytes of the page pool (0 on bad arguments; the pointer is ignored). */
+KVQ_API size_t kvq_paged_bytes(const kvq_paged_cache* cache);
+
+/*
+ * One scheduling step's bookkeeping on the device, in one launch.  Request b
+ * has ctx_lens[b] cached tokens and gets new_lens[b] new ones (negative counts
+ * are taken as 0).
+ *  1. Requests with done[b] != 0 give back the pages of their ctx_lens[b]
+ *     tokens: the pages are pushed on the free stack (free_pages[0 ..
+ *     *free_count) are the free pages) in request order, page order within a
+ *     request; their cached length becomes 0.  done may be NULL.
+ *  2. A request is served when its tokens fit its block-table row
+ *     (ctx + new <= max_pages * page_tokens), its new tokens fit the slot
+ *     array (cu_new[b + 1] <= n_slots), and it needs no page or the pages
+ *     needed by the requests up to and including it (those that fit) do not
+ *     exceed the free pages.  Pages are popped from the top of the stack in request order and written to
+ *     block_table[b][ceil(ctx / page_tokens) ...]; other entries stay as they
+ *     were.
+ *  3. The new tokens of all requests form one list, request after request:
+ *     cu_new[b] is request b's first index in it (cu_new[batch] the total,
+ *     saturated at 2^31 - 1).  slots[n] and positions[n] of list entry n are
+ *     the token's slot and its position in its request; -1 for tokens of
+ *     unserved requests and for entries behind the list.
+ *  4. seq_lens_out[b] = ctx + new for served requests, else the cached length
+ *     (so it tells which were served); *free_count_out the free pages left.
+ * ctx_lens, new_lens: device int32 [batch]; done: device int32 [batch] or NULL;
+ * block_table: device int32 [batch][max_pages] (rows of finished requests hold
+ * valid pages for their ctx_lens tokens); free_pages: device int32 [num_pages];
+ * free_count, free_count_out: device int32, may be the same word; slots: device
+ * int32 [n_slots]; positions: device int32 [n_slots] or NULL; cu_new: device
+ * int32 [batch + 1]; seq_lens_out: device int32 [batch], may be ctx_lens.
+ * No other arrays may overlap.  batch up to 8192 (more: KVQ_ERR_UNSUPPORTED).
+ */
+KVQ_API kvq_status kvq_page_plan(int32_t num_pages, int32_t page_tokens, int32_t batch, const int32_t* ctx_lens,
+                                 const int32_t* new_lens, const int32_t* done, int32_t* block_table,
+                                 int32_t max_pages, int32_t* free_pages, const int32_t* free_count,
+                                 int32_t* free_count_out, int32_t* slots, int32_t* positions, int32_t n_slots,
+                                 int32_t* cu_new, int32_t* seq_lens_out, void* stream);
+
+/*
+ * Quantize n tokens' keys and values into their slots, with the arithmetic of
+ * kvq_quantize_append except that scale = fp16((max - min) * fp32(1 / L)): the
+ * product is within one unit in the last place of the quotient, so scales and
+ * codes are the same bits but for the few groups (under 1 in 10,000) whose
+ * quotient lies that close to the middle of two fp16 numbers.
+ *  k_new, v_new: device rows of `dtype`, token t's head h at element
+ *  t * k_stride + h * 128 (t * v_stride + h * 128), e.g. slices of a fused
+ *  projection; strides in elements, at least kv_heads * 128, bases and row
+ *  starts 16-byte aligned.
+ *  slots: device int32 [n]; a slot outside the pool (-1: padding) skips its
+ *  token.  The slots inside the pool must be distinct.  No other token's bytes
+ *  change.  n == 0 is a no-op.
+ */
+KVQ_API kvq_status kvq_paged_append(const kvq_paged_cache* cache, const void* k_new, int64_t k_stride,
+                                    const void* v_new, int64_t v_stride, kvq_dtype dtype, int32_t n,
+                                    const int32_t* slots, void* stream);
+
+/*
+ * Read n cached tokens back as dense rows: x = scale * code + zero (channel 0
+ * of keys from its bf16 copy when kept), with rotate_back != 0 taken back
+ * through the orthonormal transform (keys when rotate_k, values when rotate_v;
+ * fp32 butterflies), rounded once to `dtype`.
+ *  k_out, v_out: device [n][kv_heads][128] of `dtype`, 16-byte aligned; either
+ *  may be NULL (not read back).  slots as in kvq_paged_append, repetitions
+ *  allowed; rows of slots outside the pool are zero.  n == 0 is a no-op.
+ */
+KVQ_API kvq_status kvq_paged_gather(const kvq_paged_cache* cache, const int32_t* slots, int32_t n, kvq_dtype dtype,
+                                    int32_t rotate_back, void* k_out, void* v_out, void* stream);
+
+/* Device workspace bytes kvq_paged_decode needs (0 on bad arguments). */
+KVQ_API size_t kvq_paged_decode_workspace_bytes(const kvq_paged_cache* cache, int32_t batch, int32_t q_heads);
+
+/*
+ * Decode attention of one new token per request over its pages: the scores and
+ * sums of kvq_decode_attention with the tokens taken from
+ * block_table[b][n / page_tokens].  Any GQA group size q_heads / kv_heads from
+ * 1 to 16.
+ *  q:    device rows of `dtype`, request b's head j at element
+ *        b * q_stride + j * 128 (un-rotated); 16-byte aligned rows.
+ *  block_table: device int32 [batch][max_pages]; tokens of an entry outside
+ *        [0, num_pages) take no part.
+ *  seq_lens: device int32 [batch], clamped to [0, max_len]; max_len <=
+ *        max_pages * page_tokens (larger: KVQ_ERR_CAPACITY).  A request with no
+ *        token gets a zero row.
+ *  mask: device uint32 [batch][kv_heads] kept channel groups, as
+ *        kvq_select_channels writes it, or NULL = all; only kept rows are read.
+ *  out:  device [batch][q_heads][128] of `dtype`.  For 16-bit types the
+ *        probabilities are rounded to fp16 before the value sums; for fp32 they
+ *        keep 22 bits.
+ *  workspace: device scratch, 256-byte aligned, not read by later calls (but
+ *        two calls that may run at the same time need one each).
+ */
+KVQ_API kvq_status kvq_paged_decode(const kvq_paged_cache* cache, const void* q, int64_t q_stride, kvq_dtype dtype,
+                                    int32_t q_heads, int32_t batch, const int32_t* block_table, int32_t max_pages,
+                                    const int32_t* seq_lens, int32_t max_len, const uint32_t* mask,
+                                    float softmax_scale, void* out, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/*
+ * As kvq_decode_status, for the last kvq_paged_decode that used `workspace`:
+ * KVQ_ERR_TIMEOUT when a bounded wait of it gave up (the affected outputs are
+ * NaN).  Synchronizes the stream.
+ */
+KVQ_API kvq_status kvq_paged_decode_status(const kvq_paged_cache* cache, int32_t batch, int32_t q_heads,
+                                           const void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 KVQ_API const char* kvq_status_string(kvq_status status);
 

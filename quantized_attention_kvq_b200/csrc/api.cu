@@ -5,29 +5,12 @@
 #include <cstdint>
 #include <mutex>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "api_util.cuh"
+#include "paged.cuh"
 #include "transform.cuh"
 
 namespace kvq {
 namespace {
-
-// One NVTX range per enqueueing ABI call (named after it), so that a
-// timeline profiler shows which call enqueued which kernels.  NVTX is
-// header-only and costs a branch when no tool is attached.
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
-constexpr size_t kAlign = 256;
-
-inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline size_t dtype_size(kvq_dtype t) { return t == KVQ_F32 ? 4 : 2; }
-inline bool dtype_ok(int t) { return t == KVQ_F32 || t == KVQ_BF16 || t == KVQ_F16; }
 
 // Shape/flag checks that do not look at pointers.
 kvq_status check_shape(const kvq_cache* c) {
@@ -105,8 +88,6 @@ CacheView view(const kvq_cache* c) {
   return v;
 }
 
-double inv_sqrt_d() { return 1.0 / std::sqrt((double)kHeadDim); }
-
 // Buckets of a bucket-relative RoPE cache (1 without): the arrays are those of
 // a cache of batch B * nb and capacity bucket_tokens.
 inline int n_buckets(const kvq_cache* c) { return c->bucket_tokens > 0 ? c->capacity / c->bucket_tokens : 1; }
@@ -182,8 +163,6 @@ int take_withheld_tile() {
   g_withheld_tile = -1;
   return t;
 }
-
-kvq_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
 
 // which halves of the decode to enqueue
 enum { kRunSplit = 1, kRunCombine = 2 };
@@ -520,7 +499,8 @@ KVQ_API uint32_t kvq_bounds_violations(int32_t reset) {
 #ifdef KVQ_BOUNDS_CHECK
   if (cudaDeviceSynchronize() != cudaSuccess) return UINT32_MAX;
   const bool r = reset != 0;
-  return kvq::bounds_append(r) + kvq::bounds_decode(r) + kvq::bounds_window(r);
+  return kvq::bounds_append(r) + kvq::bounds_decode(r) + kvq::bounds_window(r) + kvq::bounds_paged_append(r) +
+         kvq::bounds_paged_gather(r) + kvq::bounds_paged_decode(r);
 #else
   (void)reset;
   return UINT32_MAX;  // this build has no bounds checks

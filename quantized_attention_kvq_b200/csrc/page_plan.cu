@@ -1,0 +1,196 @@
+// One scheduling step's block tables and slot map, in one launch.
+//
+// Three prefix sums over the requests carry everything: new tokens (the flat
+// token list), pages needed (places on the free stack) and pages given back
+// (places the finished requests push to).  The j-th page of the step is
+// free_pages[top - 1 - j], top = count + pages given back, so which request gets
+// which page is known to every thread from the sums alone.
+//
+// Latency-bound: a step touches a few KB to a few MB.  One cluster of CTAs (one
+// CTA for a small step) shares the work; every CTA makes the three sums for
+// itself in shared memory (cheaper than passing them on), pushes its share of
+// the returned pages, meets the others at the cluster barrier, and then fills
+// its share of the table entries and slots, each found by a binary search in
+// the sums.  The barrier also separates reading *free_count, ctx_lens and the
+// finished requests' table rows from writing them, so they may be updated in
+// place.
+// Measured on B200, launched back to back: see kSmall below.
+#include <cooperative_groups.h>
+
+#include "paged.cuh"
+
+namespace kvq {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanCtas = 8;  // the portable cluster size
+
+// last b with sum[b] <= x, for 0 <= x < sum[n]
+__device__ __forceinline__ int find(const int* sum, int n, int x) {
+  int lo = 0, hi = n;  // sum[lo] <= x < sum[hi]
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (sum[m] <= x)
+      lo = m;
+    else
+      hi = m;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int pages_for(int tokens, int P) { return tokens / P + (tokens % P != 0); }
+
+__global__ void __launch_bounds__(kPlanThreads) k_page_plan(PlanArgs a) {
+  extern __shared__ int sm[];
+  const int B = a.batch, P = a.page_tokens, tid = threadIdx.x;
+  int* cu = sm;                 // [B + 1] new tokens before request b
+  int* need = cu + B + 1;       // [B + 1] pages needed before request b
+  int* give = need + B + 1;     // [B + 1] pages given back before request b
+  int* ctx = give + B + 1;      // [B] cached tokens, 0 for finished requests
+  __shared__ long long wsum[3][kPlanThreads / 32];
+  __shared__ int taken_s;
+  const int count = min(max(*a.count, 0), a.num_pages);
+
+  // each thread sums a run of consecutive requests; the runs are joined by a
+  // scan over the threads.  Sums are 64-bit and saturate when stored.
+  const int per = (B + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
+  constexpr long long kMax = 0x7FFFFFFF;
+  long long s[3] = {0, 0, 0};
+  const long long row_tokens = (long long)a.max_pages * P;
+  // pass 0: new tokens and pages given back; pass 1: pages needed, which depend on cu
+  for (int pass = 0; pass < 2; ++pass) {
+    long long t0 = 0, t1 = 0;
+    for (int b = b0; b < b1; ++b) {
+      if (pass == 0) {
+        const bool fin = a.done && a.done[b] != 0;
+        const int c = max(a.ctx[b], 0);
+        t0 += max(a.add[b], 0);
+        t1 += fin ? min(pages_for(c, P), a.max_pages) : 0;
+        ctx[b] = fin ? 0 : c;
+      } else {
+        const long long end = (long long)ctx[b] + max(a.add[b], 0);
+        const bool fits = end <= row_tokens && cu[b + 1] <= a.n_slots;
+        t0 += fits ? pages_for((int)end, P) - pages_for(ctx[b], P) : 0;
+      }
+    }
+    long long x0 = t0, x1 = t1;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long y0 = __shfl_up_sync(kFull, x0, m), y1 = __shfl_up_sync(kFull, x1, m);
+      if ((tid & 31) >= m) {
+        x0 += y0;
+        x1 += y1;
+      }
+    }
+    if ((tid & 31) == 31) {
+      wsum[0][tid >> 5] = x0;
+      wsum[1][tid >> 5] = x1;
+    }
+    __syncthreads();
+    s[0] = x0 - t0;
+    s[1] = x1 - t1;
+    for (int w = 0; w < (tid >> 5); ++w) {
+      s[0] += wsum[0][w];
+      s[1] += wsum[1][w];
+    }
+    int* out0 = pass == 0 ? cu : need;
+    if (tid == 0) {
+      out0[0] = 0;
+      if (pass == 0) give[0] = 0;
+      taken_s = 0;
+    }
+    for (int b = b0; b < b1; ++b) {
+      if (pass == 0) {
+        const bool fin = a.done && a.done[b] != 0;
+        s[0] += max(a.add[b], 0);
+        s[1] += fin ? min(pages_for(max(a.ctx[b], 0), P), a.max_pages) : 0;
+        cu[b + 1] = (int)min(s[0], kMax);
+        give[b + 1] = (int)min(s[1], kMax);
+      } else {
+        const long long end = (long long)ctx[b] + max(a.add[b], 0);
+        const bool fits = end <= row_tokens && cu[b + 1] <= a.n_slots;
+        s[0] += fits ? pages_for((int)end, P) - pages_for(ctx[b], P) : 0;
+        need[b + 1] = (int)min(s[0], kMax);
+      }
+    }
+    __syncthreads();
+  }
+  const int returned = give[B];
+  const int top = (int)min((long long)count + returned, (long long)a.num_pages);
+
+  // pages taken: the largest prefix of needed pages that the stack covers
+  int mine = 0;
+  for (int b = b0; b < b1; ++b)
+    if (need[b + 1] <= top) mine = max(mine, need[b + 1]);
+  mine = __reduce_max_sync(kFull, mine);
+  if ((tid & 31) == 0) atomicMax(&taken_s, mine);
+
+  const int gt = blockIdx.x * kPlanThreads + tid, gn = gridDim.x * kPlanThreads;
+  for (int r = gt; r < returned; r += gn) {
+    const int b = find(give, B, r);
+    if (count + r < a.num_pages) a.free_pages[count + r] = a.table[(size_t)b * a.max_pages + (r - give[b])];
+  }
+  if (gridDim.x > 1)
+    cg::this_cluster().sync();  // pushed pages visible; every CTA has read what is updated in place
+  else
+    __syncthreads();
+  const int taken = taken_s;
+
+  for (int j = gt; j < taken; j += gn) {
+    const int b = find(need, B, j);
+    a.table[(size_t)b * a.max_pages + pages_for(ctx[b], P) + (j - need[b])] = a.free_pages[top - 1 - j];
+  }
+  for (int n = gt; n < a.n_slots; n += gn) {
+    int slot = -1, pos = -1;
+    if (n < cu[B]) {
+      const int b = find(cu, B, n);
+      const bool fits = (long long)ctx[b] + (cu[b + 1] - cu[b]) <= row_tokens && cu[b + 1] <= a.n_slots;
+      if (fits && (need[b + 1] == need[b] || need[b + 1] <= top)) {
+        pos = ctx[b] + (n - cu[b]);
+        const int pg = pos / P, held = pages_for(ctx[b], P);
+        const int page = pg < held ? a.table[(size_t)b * a.max_pages + pg] : a.free_pages[top - 1 - (need[b] + pg - held)];
+        slot = page * P + pos % P;
+      }
+    }
+    a.slots[n] = slot;
+    if (a.positions) a.positions[n] = pos;
+  }
+  for (int b = gt; b <= B; b += gn) {
+    a.cu[b] = cu[b];
+    if (b == B) break;
+    const long long end = (long long)ctx[b] + (cu[b + 1] - cu[b]);
+    const bool fits = end <= row_tokens && cu[b + 1] <= a.n_slots;
+    a.lens[b] = fits && (need[b + 1] == need[b] || need[b + 1] <= top) ? (int)end : ctx[b];
+  }
+  if (gt == 0) *a.count_out = top - taken;
+}
+
+}  // namespace
+
+cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t s) {
+  const size_t smem = sizeof(int) * (4 * (size_t)a.batch + 3);
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(k_page_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  // a small step is one CTA's work: a cluster would only add its barrier
+  constexpr int kSmall = 4 * kPlanThreads;
+  const int ctas = (long long)a.n_slots + a.batch > kSmall ? kPlanCtas : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k_page_plan, a);
+}
+
+}  // namespace kvq

@@ -25,10 +25,12 @@ SYMBOLS = ("kvq_cache_sizes", "kvq_window_bytes", "kvq_quantize_append", "kvq_se
            "kvq_decode_step_workspace_bytes",
            "kvq_decode_step_host", "kvq_decode_attention_static", "kvq_decode_attention_select",
            "kvq_decode_partials_select", "kvq_decode_status", "kvq_test_withhold_tile", "kvq_bounds_violations",
-           "kvq_status_string")
+           "kvq_status_string", "kvq_paged_bytes", "kvq_page_plan", "kvq_paged_append", "kvq_paged_gather",
+           "kvq_paged_decode_workspace_bytes", "kvq_paged_decode", "kvq_paged_decode_status")
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 
 
 class KvqCacheStruct(ctypes.Structure):
@@ -38,6 +40,13 @@ class KvqCacheStruct(ctypes.Structure):
                 ("k_codes", _P), ("k_scales", _P), ("k_ch0", _P), ("v_codes", _P), ("v_scales", _P),
                 ("sink_tokens", _I32), ("recent_tokens", _I32), ("k_window", _P), ("v_window", _P),
                 ("t_query", _P), ("t_key", _P), ("bucket_tokens", _I32), ("rope_inv_freq", _P)]
+
+
+class KvqPagedStruct(ctypes.Structure):
+    _fields_ = [("num_pages", _I32), ("page_tokens", _I32), ("kv_heads", _I32), ("head_dim", _I32),
+                ("k_bits", _I32), ("v_bits", _I32), ("group_size", _I32), ("prune_granule", _I32),
+                ("rotate_k", _I32), ("keep_ch0", _I32), ("rotate_v", _I32), ("v_clip", ctypes.c_float),
+                ("pages", _P)]
 
 
 class KvqError(RuntimeError):
@@ -95,6 +104,22 @@ def lib():
         L.kvq_bounds_violations.restype = ctypes.c_uint32
         L.kvq_test_withhold_tile.argtypes = [_I32]
         L.kvq_test_withhold_tile.restype = None
+        D = ctypes.POINTER(KvqPagedStruct)
+        L.kvq_paged_bytes.argtypes = [D]
+        L.kvq_paged_bytes.restype = ctypes.c_size_t
+        L.kvq_page_plan.argtypes = [_I32, _I32, _I32, _P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _I32, _P, _P, _P]
+        L.kvq_page_plan.restype = ctypes.c_int
+        L.kvq_paged_append.argtypes = [D, _P, _I64, _P, _I64, ctypes.c_int, _I32, _P, _P]
+        L.kvq_paged_append.restype = ctypes.c_int
+        L.kvq_paged_gather.argtypes = [D, _P, _I32, ctypes.c_int, _I32, _P, _P, _P]
+        L.kvq_paged_gather.restype = ctypes.c_int
+        L.kvq_paged_decode_workspace_bytes.argtypes = [D, _I32, _I32]
+        L.kvq_paged_decode_workspace_bytes.restype = ctypes.c_size_t
+        L.kvq_paged_decode.argtypes = [D, _P, _I64, ctypes.c_int, _I32, _I32, _P, _I32, _P, _I32, _P, ctypes.c_float,
+                                       _P, _P, ctypes.c_size_t, _P]
+        L.kvq_paged_decode.restype = ctypes.c_int
+        L.kvq_paged_decode_status.argtypes = [D, _I32, _I32, _P, ctypes.c_size_t, _P]
+        L.kvq_paged_decode_status.restype = ctypes.c_int
         L.kvq_status_string.argtypes = [ctypes.c_int]
         L.kvq_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -110,8 +135,11 @@ def _check(status: int, what: str):
         raise KvqError(status, what)
 
 
+_DTYPE_CODES = {torch.float32: KVQ_F32, torch.bfloat16: KVQ_BF16, torch.float16: KVQ_F16}
+
+
 def torch_dtype_code(t: torch.dtype) -> int:
-    return {torch.float32: KVQ_F32, torch.bfloat16: KVQ_BF16, torch.float16: KVQ_F16}[t]
+    return _DTYPE_CODES[t]
 
 
 def _dev_ptr(t: torch.Tensor | None) -> int | None:
@@ -327,3 +355,189 @@ class KVQCache:
                                           float(softmax_scale), out_host.data_ptr(), _dev_ptr(workspace),
                                           workspace.numel(), _stream(stream)),
                "kvq_decode_step_host")
+
+
+def _device_of(*tensors: torch.Tensor | None) -> int:
+    """Index of the one CUDA device all the tensors are on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        d = t.get_device()  # -1 for a host tensor
+        if d < 0:
+            raise ValueError("expected a CUDA tensor (the library has no CPU path)")
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"tensors on cuda:{dev} and cuda:{d}")
+    return dev
+
+
+def _i32(t: torch.Tensor | None, name: str, *shape: int) -> int | None:
+    """Pointer of a contiguous int32 tensor of a given shape."""
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} is a contiguous int32 tensor of shape {list(shape)}")
+    return t.data_ptr()
+
+
+def _call(dev: int, stream, what: str, fn, *args):
+    """One library call on the tensors' device, on its current stream or the caller's."""
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != KVQ_OK:
+        raise KvqError(status, what)
+
+
+def _rows(t: torch.Tensor, name: str, heads: int) -> tuple[int, int]:
+    """(pointer, row stride in elements) of [rows][heads][128] with contiguous heads."""
+    if t.dim() != 3 or t.shape[1:] != (heads, 128):
+        raise ValueError(f"{name} is [rows][{heads}][128]")
+    n, (a, b, c) = t.shape[0], t.stride()
+    if n and (c != 1 or (heads > 1 and b != 128)):
+        raise ValueError(f"{name}: a row's heads and channels are contiguous")
+    return t.data_ptr(), a if n > 1 else heads * 128
+
+
+class PagePlan:
+    """What a scheduling step's plan wrote (see PagePlanner.plan)."""
+
+    __slots__ = ("slots", "positions", "cu_new", "seq_lens", "free_count")
+
+    def __init__(self, slots, positions, cu_new, seq_lens, free_count):
+        self.slots, self.positions, self.cu_new = slots, positions, cu_new
+        self.seq_lens, self.free_count = seq_lens, free_count
+
+
+class PagePlanner:
+    """Block tables and slot maps of a page pool, built on the device (kvq_page_plan)."""
+
+    def __init__(self, num_pages: int, page_tokens: int = 64):
+        self.num_pages, self.page_tokens = num_pages, page_tokens
+
+    def plan(self, ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+             free_pages: torch.Tensor, free_count: torch.Tensor, n_slots: int, done: torch.Tensor | None = None,
+             out: PagePlan | None = None, stream=None) -> PagePlan:
+        """ctx_lens, new_lens, done: int32 [B]; block_table: int32 [B][max_pages] and free_pages: int32
+        [num_pages], both updated in place; free_count: int32 [1].  Returns the new tokens' slots and
+        positions [n_slots], cu_new [B + 1], the sequence lengths [B] and the free pages left [1]; `out`
+        reuses an earlier plan's tensors (its seq_lens may be ctx_lens, its free_count free_count)."""
+        if ctx_lens.dim() != 1 or block_table.dim() != 2:
+            raise ValueError("ctx_lens is [B], block_table [B][max_pages]")
+        B, max_pages = block_table.shape
+        ctx = _i32(ctx_lens, "ctx_lens", B)
+        if out is None:
+            out = PagePlan(ctx_lens.new_empty(n_slots), ctx_lens.new_empty(n_slots), ctx_lens.new_empty(B + 1),
+                           ctx_lens.new_empty(B), ctx_lens.new_empty(1))
+        dev = _device_of(ctx_lens, new_lens, block_table, free_pages, free_count, done, out.slots, out.positions,
+                         out.cu_new, out.seq_lens, out.free_count)
+        _call(dev, stream, "kvq_page_plan", lib().kvq_page_plan, self.num_pages, self.page_tokens, B, ctx,
+              _i32(new_lens, "new_lens", B), _i32(done, "done", B), _i32(block_table, "block_table", B, max_pages),
+              max_pages, _i32(free_pages, "free_pages", self.num_pages), _i32(free_count, "free_count", 1),
+              _i32(out.free_count, "free_count", 1), _i32(out.slots, "slots", n_slots),
+              _i32(out.positions, "positions", n_slots), n_slots, _i32(out.cu_new, "cu_new", B + 1),
+              _i32(out.seq_lens, "seq_lens", B))
+        return out
+
+
+class PagedKVQCache:
+    """Page pool of packed quantized keys and values in device memory (torch-allocated, library-laid-out)."""
+
+    def __init__(self, num_pages: int, H: int, k_bits: int, v_bits: int, page_tokens: int = 64, rotate_k: int = 1,
+                 keep_ch0: int = 0, rotate_v: int = 0, v_clip: float = 1.0, device="cuda",
+                 pages: torch.Tensor | None = None):
+        """pages: the pool's memory when the caller owns it (uint8, at least kvq_paged_bytes bytes, kept
+        referenced here); allocated and zeroed otherwise."""
+        self.desc = KvqPagedStruct(num_pages, page_tokens, H, 128, k_bits, v_bits, 32, 4, rotate_k, keep_ch0, rotate_v,
+                                   v_clip)
+        self._ref = ctypes.byref(self.desc)
+        self.bytes = lib().kvq_paged_bytes(self._ref)
+        if self.bytes == 0:
+            raise KvqError(KVQ_ERR_UNSUPPORTED, "kvq_paged_bytes")
+        if pages is None:
+            pages = torch.zeros(self.bytes, dtype=torch.uint8, device=device)
+        if pages.dtype != torch.uint8 or pages.numel() < self.bytes:
+            raise ValueError(f"pages: at least {self.bytes} bytes (uint8)")
+        self.pages = pages
+        self.desc.pages = _dev_ptr(pages)
+        self.num_pages, self.H, self.page_tokens = num_pages, H, page_tokens
+        self.planner = PagePlanner(num_pages, page_tokens)
+
+    def append(self, k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor, stream=None):
+        """k_new, v_new: [n][H][128] (fp32 / bf16 / fp16), rows at any 16-byte stride; slots: int32 [n]."""
+        dev = _device_of(k_new, v_new, slots, self.pages)
+        if k_new.dtype != v_new.dtype or k_new.shape != v_new.shape:
+            raise ValueError("k_new and v_new have one type and shape")
+        k, ks = _rows(k_new, "k_new", self.H)
+        v, vs = _rows(v_new, "v_new", self.H)
+        n = k_new.shape[0]
+        _call(dev, stream, "kvq_paged_append", lib().kvq_paged_append, self._ref, k, ks, v, vs,
+              torch_dtype_code(k_new.dtype), n, _i32(slots, "slots", n))
+
+    def gather(self, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16, rotate_back: bool = True,
+               k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, stream=None):
+        """The cached tokens' keys and values as dense rows [n][H][128] of `dtype`."""
+        n, shape = slots.shape[0], (slots.shape[0], self.H, 128)
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype, device=slots.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=dtype, device=slots.device)
+        for t in (k_out, v_out):
+            if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+                raise ValueError(f"k_out and v_out are contiguous {list(shape)} of {dtype}")
+        dev = _device_of(slots, k_out, v_out, self.pages)
+        _call(dev, stream, "kvq_paged_gather", lib().kvq_paged_gather, self._ref, _i32(slots, "slots", n), n,
+              torch_dtype_code(dtype), int(rotate_back), k_out.data_ptr(), v_out.data_ptr())
+        return k_out, v_out
+
+    def select(self, q: torch.Tensor, keep_groups: int, mask_out: torch.Tensor | None = None, stream=None):
+        """q: [B][Hq][128] contiguous; the kept channel groups [B][H] (int32 bits) for decode's mask
+        (kvq_select_channels)."""
+        dev = _device_of(q, mask_out, self.pages)
+        if q.dim() != 3 or q.shape[2] != 128 or not q.is_contiguous():
+            raise ValueError("q is a contiguous [B][Hq][128]")
+        if mask_out is None:
+            mask_out = torch.empty((q.shape[0], self.H), dtype=torch.int32, device=q.device)
+        d = describe(q.shape[0], self.H, 128, self.desc.k_bits, self.desc.v_bits, self.desc.rotate_k,
+                     self.desc.keep_ch0)
+        _call(dev, stream, "kvq_select_channels", lib().kvq_select_channels, ctypes.byref(d), q.data_ptr(),
+              torch_dtype_code(q.dtype), q.shape[1], keep_groups, _i32(mask_out, "mask_out", q.shape[0], self.H))
+        return mask_out
+
+    def workspace_bytes(self, batch: int, q_heads: int) -> int:
+        return lib().kvq_paged_decode_workspace_bytes(self._ref, batch, q_heads)
+
+    def decode(self, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, max_len: int,
+               mask: torch.Tensor | None = None, softmax_scale: float | None = None, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """q: [B][Hq][128], rows at any 16-byte stride; block_table: int32 [B][max_pages]; seq_lens: int32 [B];
+        returns [B][Hq][128] of q's type."""
+        if q.dim() != 3 or block_table.dim() != 2:
+            raise ValueError("q is [B][Hq][128], block_table [B][max_pages]")
+        B, Hq = q.shape[0], q.shape[1]
+        qp, qs = _rows(q, "q", Hq)
+        if out is None:
+            out = torch.empty((B, Hq, 128), dtype=q.dtype, device=q.device)
+        elif out.shape != (B, Hq, 128) or out.dtype is not q.dtype or not out.is_contiguous():
+            raise ValueError(f"out is a contiguous [{B}][{Hq}][128] of {q.dtype}")
+        if workspace is None:
+            workspace = torch.empty(max(self.workspace_bytes(B, Hq), 256), dtype=torch.uint8, device=q.device)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace is contiguous")
+        dev = _device_of(q, block_table, seq_lens, mask, out, workspace, self.pages)
+        max_pages = block_table.shape[1]
+        _call(dev, stream, "kvq_paged_decode", lib().kvq_paged_decode, self._ref, qp, qs, torch_dtype_code(q.dtype), Hq,
+              B, _i32(block_table, "block_table", B, max_pages), max_pages, _i32(seq_lens, "seq_lens", B), max_len,
+              _i32(mask, "mask", B, self.H), 0.08838834764831845 if softmax_scale is None else softmax_scale,
+              out.data_ptr(), workspace.data_ptr(), workspace.nbytes)
+        return out
+
+    def decode_status(self, batch: int, q_heads: int, workspace: torch.Tensor, stream=None) -> int:
+        """Status of the last decode that used `workspace`: KVQ_OK or KVQ_ERR_TIMEOUT (synchronizes the stream)."""
+        return lib().kvq_paged_decode_status(self._ref, batch, q_heads, _dev_ptr(workspace),
+                                             workspace.nbytes, _stream(stream))
