@@ -24,7 +24,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 1024;
 constexpr int kPlanCtas = 8;  // the portable cluster size
 
 // last b with sum[b] <= x, for 0 <= x < sum[n]
@@ -143,20 +143,50 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PlanArgs a) {
     const int b = find(need, B, j);
     a.table[(size_t)b * a.max_pages + pages_for(ctx[b], P) + (j - need[b])] = a.free_pages[top - 1 - j];
   }
-  for (int n = gt; n < a.n_slots; n += gn) {
-    int slot = -1, pos = -1;
-    if (n < cu[B]) {
-      const int b = find(cu, B, n);
-      const bool fits = (long long)ctx[b] + (cu[b + 1] - cu[b]) <= row_tokens && cu[b + 1] <= a.n_slots;
-      if (fits && (need[b + 1] == need[b] || need[b + 1] <= top)) {
-        pos = ctx[b] + (n - cu[b]);
-        const int pg = pos / P, held = pages_for(ctx[b], P);
-        const int page = pg < held ? a.table[(size_t)b * a.max_pages + pg] : a.free_pages[top - 1 - (need[b] + pg - held)];
-        slot = page * P + pos % P;
+  // a thread takes four consecutive list entries: one search, then steps to the
+  // next request; entries on one page share its look-up
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
+  for (int n0 = 4 * gt; n0 < a.n_slots; n0 += 4 * gn) {
+    int slot[4], pos[4];
+    int b = n0 < cu[B] ? find(cu, B, n0) : B;
+    int first = -1, p = 0, off = P, page = 0, held = 0;  // the request the rest is about; next position, its place in its page
+    bool served = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int n = n0 + k;
+      slot[k] = pos[k] = -1;
+      if (n >= a.n_slots || n >= cu[B]) continue;
+      while (n >= cu[b + 1]) ++b;
+      int pg = -1;  // the page to look up
+      if (b != first) {
+        first = b;
+        held = pages_for(ctx[b], P);
+        const bool fits = (long long)ctx[b] + (cu[b + 1] - cu[b]) <= row_tokens && cu[b + 1] <= a.n_slots;
+        served = fits && (need[b + 1] == need[b] || need[b + 1] <= top);
+        p = ctx[b] + (n - cu[b]);
+        pg = p / P;
+        off = p - pg * P;
+      } else if (off == P) {
+        pg = p / P;
+        off = 0;
+      }
+      if (!served) continue;
+      if (pg >= 0)
+        page = pg < held ? a.table[(size_t)b * a.max_pages + pg] : a.free_pages[top - 1 - (need[b] + pg - held)];
+      slot[k] = page * P + off;
+      pos[k] = p;
+      ++p;
+      ++off;
+    }
+    if (wide && n0 + 4 <= a.n_slots) {
+      *reinterpret_cast<int4*>(a.slots + n0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      if (a.positions) *reinterpret_cast<int4*>(a.positions + n0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+      for (int k = 0; k < 4 && n0 + k < a.n_slots; ++k) {
+        a.slots[n0 + k] = slot[k];
+        if (a.positions) a.positions[n0 + k] = pos[k];
       }
     }
-    a.slots[n] = slot;
-    if (a.positions) a.positions[n] = pos;
   }
   for (int b = gt; b <= B; b += gn) {
     a.cu[b] = cu[b];

@@ -99,11 +99,19 @@ struct PagedDecodeArgs {
   float* part_acc;   // [units + ranks][G][128] unnormalized sums
   float2* part_ml;   // [units + ranks][G] (running max, running sum)
   int32_t* starts;   // [B + 1] first tile of each request, times H
-  int32_t* status;   // [ranks] 1 where a bounded wait of the rank gave up
+  int32_t* status;   // [kPagedMaxRanks] 1 where a bounded wait of the rank gave up
   size_t part_rows;
 };
-// ranks (warps) the tiles of a decode with G query heads per kv head are spread over
-int paged_decode_ranks(const PagedView& c, int G, int dtype);
+// The tiles of a decode are spread over ranks: the warps of one CTA per SM.  More
+// warps hide more latency, as long as their registers do not spill.
+constexpr int kPagedSms = 148;
+constexpr int paged_decode_warps(int padded_heads, bool f32) {
+  return f32 || padded_heads == 16 ? 8 : padded_heads == 8 ? 12 : 16;
+}
+constexpr int kPagedMaxRanks = 16 * kPagedSms;
+inline int paged_decode_ranks(int G, int dtype) {
+  return kPagedSms * paged_decode_warps(G <= 4 ? 4 : G <= 8 ? 8 : 16, dtype == KVQ_F32);
+}
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t s);
 
 unsigned bounds_paged_append(bool reset);

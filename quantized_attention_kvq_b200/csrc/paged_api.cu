@@ -19,6 +19,8 @@ kvq_status check_paged_shape(const kvq_paged_cache* c) {
   if ((c->k_bits != 2 && c->k_bits != 4) || (c->v_bits != 2 && c->v_bits != 4)) return KVQ_ERR_UNSUPPORTED;
   if (c->page_tokens % kBlockTokens != 0 || c->page_tokens > kMaxPageTokens) return KVQ_ERR_UNSUPPORTED;
   if ((int64_t)c->num_pages * c->page_tokens > INT32_MAX || c->kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  if ((int64_t)c->num_pages * (c->page_tokens / kBlockTokens) * c->kv_heads > INT32_MAX)
+    return KVQ_ERR_UNSUPPORTED;  // blocks are numbered in 32 bits (12 TB of pool)
   return KVQ_OK;
 }
 
@@ -53,18 +55,15 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 // tiles, and one status word per rank.
 struct PagedPlan {
   size_t rows, ml_offset, starts_offset, status_offset, bytes;
-  int ranks;
 };
 
-PagedPlan plan_paged(const kvq_paged_cache* c, int32_t batch, int32_t q_heads, int32_t dtype) {
+PagedPlan plan_paged(const kvq_paged_cache* c, int32_t batch, int32_t q_heads) {
   PagedPlan p;
-  const int G = q_heads / c->kv_heads;
-  p.ranks = paged_decode_ranks(paged_view(c), G, dtype);
-  p.rows = ((size_t)batch * c->kv_heads + p.ranks) * G;
+  p.rows = ((size_t)batch * c->kv_heads + kPagedMaxRanks) * (q_heads / c->kv_heads);
   p.ml_offset = round_up(p.rows * kHeadDim * sizeof(float), kAlign);
   p.starts_offset = p.ml_offset + round_up(p.rows * sizeof(float2), kAlign);
   p.status_offset = p.starts_offset + round_up(((size_t)batch + 1) * sizeof(int32_t), kAlign);
-  p.bytes = p.status_offset + round_up((size_t)p.ranks * sizeof(int32_t), kAlign);
+  p.bytes = p.status_offset + round_up(kPagedMaxRanks * sizeof(int32_t), kAlign);
   return p;
 }
 
@@ -174,7 +173,7 @@ KVQ_API kvq_status kvq_paged_gather(const kvq_paged_cache* c, const int32_t* slo
 
 KVQ_API size_t kvq_paged_decode_workspace_bytes(const kvq_paged_cache* c, int32_t batch, int32_t q_heads) {
   if (check_paged_shape(c) != KVQ_OK || check_paged_heads(c, batch, q_heads) != KVQ_OK) return 0;
-  return plan_paged(c, batch, q_heads, KVQ_F32).bytes;
+  return plan_paged(c, batch, q_heads).bytes;
 }
 
 KVQ_API kvq_status kvq_paged_decode(const kvq_paged_cache* c, const void* q, int64_t q_stride, kvq_dtype dtype,
@@ -194,7 +193,7 @@ KVQ_API kvq_status kvq_paged_decode(const kvq_paged_cache* c, const void* q, int
   if (max_len > (int64_t)max_pages * c->page_tokens) return KVQ_ERR_CAPACITY;
   const int64_t tiles = ((int64_t)max_len + kBlockTokens - 1) / kBlockTokens;
   if (tiles * batch * c->kv_heads > INT32_MAX) return KVQ_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
-  const PagedPlan p = plan_paged(c, batch, q_heads, dtype);
+  const PagedPlan p = plan_paged(c, batch, q_heads);
   if (workspace_bytes < p.bytes) return KVQ_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   PagedDecodeArgs a;
@@ -227,17 +226,16 @@ KVQ_API kvq_status kvq_paged_decode_status(const kvq_paged_cache* c, int32_t bat
   if (st != KVQ_OK) return st;
   if ((st = check_paged_heads(c, batch, q_heads)) != KVQ_OK) return st;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0) return KVQ_ERR_INVALID_ARG;
-  const PagedPlan p = plan_paged(c, batch, q_heads, KVQ_F32);
+  const PagedPlan p = plan_paged(c, batch, q_heads);
   if (workspace_bytes < p.bytes) return KVQ_ERR_WORKSPACE;
-  int32_t words[2048];
-  if (p.ranks > (int)(sizeof(words) / sizeof(words[0]))) return KVQ_ERR_UNSUPPORTED;
+  int32_t words[kPagedMaxRanks];
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemcpyAsync(words, static_cast<const char*>(workspace) + p.status_offset, p.ranks * sizeof(int32_t),
+  if (cudaMemcpyAsync(words, static_cast<const char*>(workspace) + p.status_offset, sizeof(words),
                       cudaMemcpyDeviceToHost, s) != cudaSuccess ||
       cudaStreamSynchronize(s) != cudaSuccess)
     return KVQ_ERR_CUDA;
-  for (int i = 0; i < p.ranks; ++i)
-    if (words[i]) return KVQ_ERR_TIMEOUT;
+  for (int32_t w : words)
+    if (w) return KVQ_ERR_TIMEOUT;
   return KVQ_OK;
 }
 

@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(256) k_paged_combine(PagedDecodeArgs a, int ma
       const long long x = (long long)s0 * H + (long long)h * tiles;
       const int r0 = (int)(((x + 1) * ranks - 1) / total), r1 = (int)(((x + tiles) * ranks - 1) / total);
       const size_t unit = (size_t)b * H + h;
-      constexpr int U = 4;  // partials in flight per warp
+      constexpr int U = 8;  // partials in flight per warp
       for (int r = r0 + part; r <= r1; r += U * WPR) {
         float2 ml[U];
         float4 v[U];
@@ -123,14 +123,12 @@ __global__ void __launch_bounds__(256) k_paged_combine(PagedDecodeArgs a, int ma
 }  // namespace
 }  // namespace paged
 
-int paged_decode_ranks(const PagedView&, int, int) { return 8 * paged::kSms; }
-
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t s) {
   using namespace paged;
   cudaError_t e = a.c.k_bits == 4 ? (a.c.v_bits == 4 ? launch_44(a, s) : launch_42(a, s))
                                   : (a.c.v_bits == 4 ? launch_24(a, s) : launch_22(a, s));
   if (e != cudaSuccess) return e;
-  const int ranks = paged_decode_ranks(a.c, a.G, a.dtype);
+  const int ranks = paged_decode_ranks(a.G, a.dtype);
   // one warp per row where a row has few partials, a block per row where its
   // sequence was cut into many
   const long long units = (long long)a.B * a.c.H, rows = (long long)a.B * a.Hq;

@@ -23,11 +23,12 @@
 //           16 tokens), P' = p * scale of the token and group the 8-column one.
 //           P' goes from the score layout into the operand layout by an
 //           in-register 8x8 transpose; no shared memory is written.
-// Softmax: p = 2^(s - M) with M raised only when some p * scale would pass 2^15,
-// so P' fits fp16 and one warp vote per tile usually replaces the maxima.  The
-// sums over a tile stay in the matrix unit's fp32 accumulators and are then
-// added to fp32 registers, so a long sequence does not run up rounding in one
-// direction; the zero-point terms are fp32 FMAs.
+// Softmax: p = 2^(s - M) with M raised only when p or p * scale could pass 2^15
+// (bounds kept per warp), so both fit fp16 and one warp vote per tile usually
+// replaces the maxima.  p is rounded to fp16 once; P' and the zero-point sums,
+// one more product with the transposed zeros, both start from it.  The sums over
+// a tile stay in the matrix unit's fp32 accumulators and are then added to fp32
+// registers, so a long sequence does not run up rounding in one direction.
 //
 // Precision by output type.  The matrix unit aligns products by their nominal
 // exponents, so a subnormal operand costs it as many low bits as the code has
@@ -37,9 +38,12 @@
 // multiplies, which an fp16 output can tell: there the middle times the
 // sum of the rounded P' is subtracted by one more product per group.  For fp32
 // outputs the codes become normal fp16 numbers (a mask with an OR of 1024 and
-// one subtraction), P' keeps a second fp16 piece, and the value codes are counted
-// from their middle before the product, so that nothing cancels.
+// one subtraction), P' comes from the fp32 p and keeps a second fp16 piece, the
+// zero-point sums are fp32 FMAs, and the value codes are counted from their
+// middle before the product, so that nothing cancels.
 #pragma once
+
+#include <atomic>
 
 #include "paged.cuh"
 #include "sm100.cuh"
@@ -49,37 +53,60 @@ namespace paged {
 
 using namespace sm100;
 
-constexpr int kSms = 148;
+constexpr int kSms = kPagedSms;
 constexpr int kSmemLimit = 227 * 1024;
-constexpr int kMaxStages = 6;
-constexpr float kMStart = -1.0e30f;    // "no token yet": below any score, finite
+constexpr int kMaxSlots = 4;            // ring slots of keys, and of values, per warp
+constexpr float kMStart = -1.0e30f;     // "no token yet": below any score, finite
 constexpr float kLow = 1.0f / 2048.0f;  // weight of a low piece
+constexpr float kTop16 = 32768.0f;      // bound of p and of P'
 
-// query heads per kv head are padded to HC = 4, 8 or 16
-// MODE by the output type: how much of P' and of the codes' midpoint is kept
+// MODE by the output type: how much of P' and of the codes' middle is kept
 enum { kBf16 = 0, kF16 = 1, kF32 = 2 };
 
-template <int KB, int VB, int HC, int MODE>
+// query heads per kv head are padded to HC = 4, 8 or 16
+template <int KB, int VB, int HC, int MODE, bool CH0>
 struct Shape {
   static constexpr bool PREC = MODE == kF32;
-  static constexpr int NT = HC / 4;              // 8-column tiles of the query operand (two pieces per head)
-  static constexpr int HT = HC / 4;              // heads per thread
-  static constexpr int NP = HC == 4 ? 1 : (HC / 8) * (PREC ? 2 : 1);  // 8-column tiles of P'
+  static constexpr int NT = HC / 4;               // 8-column tiles of the query operand (two pieces per head)
+  static constexpr int HT = HC / 4;               // heads per thread
+  static constexpr int NH = HC == 4 ? 1 : HC / 8;  // 8-column tiles of heads
+  static constexpr int NP = NH * (PREC && HC > 4 ? 2 : 1);  // 8-column tiles of P'
   static constexpr bool PAIR = HC == 4 && !PREC;  // P' columns: (head, group of a pair)
   static constexpr int OC = HC == 4 ? 2 : HC / 2;  // fp32 sums per thread and 16-channel tile
-  static constexpr int WARPS = 8;
+  static constexpr int WARPS = paged_decode_warps(HC, PREC);
+  static constexpr int THREADS = 32 * WARPS;
   static constexpr int QF = 8 * NT * 256;         // query fragments: 8 K-steps
   static constexpr int QZ = NT * 128;             // per-group query sums, as a fragment
   static constexpr int QH = HC * 8;               // per head: score factor, channel 0
-  static constexpr int WARP_FIXED = QF + QZ + QH;
-  static constexpr int FIXED = 260 * 4 + 64 + WARPS * kMaxStages * 8 + WARPS * WARP_FIXED;
-  static constexpr int stage(bool ch0) { return BlockLayout(KB, VB, ch0).bytes; }
-  static constexpr int stages(bool ch0) {
-    const int fit = (kSmemLimit - FIXED - 128) / (WARPS * stage(ch0));
-    return fit < kMaxStages ? fit : kMaxStages;
+  static constexpr int TILES = 64 * 16;           // what is known of the warp's next tiles
+  static constexpr int ROWS = 32;                 // the kept key rows, one byte each
+  static constexpr int WARP_FIXED = QF + QZ + QH + TILES + ROWS;
+  static constexpr int F_WTOT = (THREADS + 4) * 4;
+  static constexpr int F_BARS = F_WTOT + 64;
+  static constexpr int F_WARP = F_BARS + WARPS * 2 * kMaxSlots * 8;
+  static constexpr int RING = (F_WARP + WARPS * WARP_FIXED + 127) / 128 * 128;
+  // a block's two parts: keys (codes, scales, zeros, channel 0) and values
+  static constexpr int K_SCALES = BlockLayout(KB, VB, CH0).ks, K_ZEROS = BlockLayout(KB, VB, CH0).kz;
+  static constexpr int K_CH0 = BlockLayout(KB, VB, CH0).k0, KPART = BlockLayout(KB, VB, CH0).vc;
+  static constexpr int V_SCALES = kBlockTokens * kHeadDim * VB / 8, V_ZEROS = V_SCALES + kScaleBytes;
+  static constexpr int VPART = V_ZEROS + kScaleBytes;
+  // ring slots per warp: as many as fit, keys first
+  static constexpr int slots(bool keys) {
+    int k = 1, v = 1;
+    const int room = (kSmemLimit - RING) / WARPS;
+    while (true) {
+      if (k <= v && k < kMaxSlots && (k + 1) * KPART + v * VPART <= room)
+        ++k;
+      else if (v < k && v < kMaxSlots && k * KPART + (v + 1) * VPART <= room)
+        ++v;
+      else
+        return keys ? k : v;
+    }
   }
-  static constexpr int smem(bool ch0) { return FIXED + 128 + WARPS * stages(ch0) * stage(ch0); }
-  static_assert(stages(true) >= 1 && stages(false) >= 1, "ring");
+  static constexpr int SK = slots(true), SV = slots(false);
+  static constexpr int WARP_RING = SK * KPART + SV * VPART;
+  static constexpr int SMEM = RING + WARPS * WARP_RING;
+  static_assert(SMEM <= kSmemLimit, "shared memory");
 };
 
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -88,16 +115,53 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(b0));
+// 16 bytes global -> shared, asynchronously; the second form arrives on a barrier
+// (counted at its initialization) when the thread's copies so far have landed
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// ... from zero
+__device__ __forceinline__ void mma16z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma8z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
 }
 // 8x8 transpose of 16-bit elements held two per lane
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
+}
+// four 8x8 matrices of 16-bit elements from shared memory, transposed: matrix
+// i's rows start at the addresses of lanes 8i .. 8i+7
+__device__ __forceinline__ uint4 load_transposed(uint32_t addr) {
+  uint4 r;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// one half of a pair in both places
+__device__ __forceinline__ uint32_t dup_half(uint32_t a, bool high) {
+  const __half2 h = *reinterpret_cast<const __half2*>(&a);
+  const __half2 r = high ? __high2half2(h) : __low2half2(h);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -123,12 +187,12 @@ __device__ __forceinline__ uint32_t codes_of(uint32_t w, uint32_t mask, int mid)
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Bounded wait (about a second); false after a give-up
+// Bounded wait of a whole warp (about a second); false after a give-up
 __device__ __forceinline__ bool wait_full(uint32_t bar, uint32_t parity) {
-  if (__builtin_expect(mbar_test_wait(bar, parity), 1)) return true;
+  if (__all_sync(kFull, mbar_test_wait(bar, parity))) return true;
 #pragma unroll 1
   for (uint32_t it = 0; it < (1u << 21); ++it)
-    if (mbar_try_wait_sleep(bar, parity, 500u)) return true;
+    if (__all_sync(kFull, mbar_try_wait_sleep(bar, parity, 500u))) return true;
   return false;
 }
 
@@ -137,31 +201,31 @@ __device__ __forceinline__ int tiles_of(const PagedDecodeArgs& a, int b) {
   return (len + kBlockTokens - 1) / kBlockTokens;
 }
 
-// What a lane knows of one tile of the warp's range
+// One tile of a warp's range, as its lanes leave it in shared memory (16 bytes)
 struct Tile {
-  const uint8_t* src;  // its block (nullptr: the page is outside the pool)
-  int nval;            // valid tokens, 0..64
-  int unit;            // request * H + head, -1 past the range
-  uint32_t msk;        // kept channel groups
+  int block;     // its block's number in the pool, -1: the page is outside the pool
+  int unit;      // request * H + head
+  uint32_t msk;  // kept channel groups
+  int nval;      // valid tokens, 0..64
 };
 
-template <int KB, int VB, int HC, int MODE>
-__global__ void __launch_bounds__(Shape<KB, VB, HC, MODE>::WARPS * 32, 1) k_paged_decode(PagedDecodeArgs a) {
-  using S = Shape<KB, VB, HC, MODE>;
+template <int KB, int VB, int HC, int MODE, bool CH0>
+__global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_paged_decode(PagedDecodeArgs a) {
+  using S = Shape<KB, VB, HC, MODE, CH0>;
   constexpr bool PREC = S::PREC;
-  constexpr int W = S::WARPS, NT = S::NT, HT = S::HT, NP = S::NP, OC = S::OC;
+  constexpr int W = S::WARPS, TH = S::THREADS, NT = S::NT, HT = S::HT, NH = S::NH, NP = S::NP, OC = S::OC;
   extern __shared__ __align__(128) uint8_t smem[];
   const PagedView& c = a.c;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the warp's number through a shuffle: the compiler then knows it to be the same
+  // in all lanes, and keeps ring and barrier addresses in uniform registers
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   const int g = lane >> 2, cq = lane & 3;
-  const bool ch0 = c.keep_ch0 != 0;
-  const BlockLayout lay(KB, VB, ch0);
-  const int ST = S::stages(ch0);
+  constexpr int SK = S::SK, SV = S::SV;
 
   // ---- tiles per request: chunk prefix sums over the batch
-  int* chunk = reinterpret_cast<int*>(smem);  // [257] tiles before each chunk of requests
-  int* wtot = chunk + 260;                    // [8]
-  const int per_chunk = (a.B + 255) / 256;
+  int* chunk = reinterpret_cast<int*>(smem);  // [TH + 1] tiles before each chunk of requests
+  int* wtot = reinterpret_cast<int*>(smem + S::F_WTOT);
+  const int per_chunk = (a.B + TH - 1) / TH;
   {
     int mine = 0;
     const int b0 = min(tid * per_chunk, a.B), b1 = min(b0 + per_chunk, a.B);
@@ -177,31 +241,38 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE>::WARPS * 32, 1) k_page
     int before = x - mine;
     for (int w = 0; w < warp; ++w) before += wtot[w];
     chunk[tid] = before;
-    if (tid == 255) chunk[256] = before + mine;
+    if (tid == TH - 1) chunk[TH] = before + mine;
     if (blockIdx.x == 0) {  // for the combine
       for (int b = b0; b < b1; ++b) {
         a.starts[b] = before;
         before += tiles_of(a, b);
       }
-      if (tid == 255) a.starts[a.B] = chunk[256];
+      if (tid == TH - 1) a.starts[a.B] = chunk[TH];
     }
-    static_assert(W == 8, "256 threads");
+    if (warp == 0 && lane == 0)  // status words of ranks other shapes have
+      for (int r = W * kSms + blockIdx.x; r < kPagedMaxRanks; r += kSms) a.status[r] = 0;
   }
-  uint8_t* fix = smem + 260 * 4 + 64;
-  const uint32_t bars = smem_addr(fix) + warp * kMaxStages * 8;
-  uint8_t* mine = fix + W * kMaxStages * 8 + warp * S::WARP_FIXED;
+  const uint32_t kbars = smem_addr(smem + S::F_BARS) + warp * 2 * kMaxSlots * 8, vbars = kbars + kMaxSlots * 8;
+  uint8_t* mine = smem + S::F_WARP + warp * S::WARP_FIXED;
   uint32_t* qf = reinterpret_cast<uint32_t*>(mine);                  // [8][NT][32] x {b0, b1}
   uint32_t* qz = reinterpret_cast<uint32_t*>(mine + S::QF);          // [NT][32]
   float2* qh = reinterpret_cast<float2*>(mine + S::QF + S::QZ);      // [HC] (factor, channel 0)
-  uint8_t* ring = smem + (S::FIXED + 127) / 128 * 128 + (size_t)warp * ST * lay.bytes;
-  for (int i = lane; i < S::WARP_FIXED / 4; i += 32) qf[i] = 0;  // columns of absent heads stay zero
+  Tile* tiles = reinterpret_cast<Tile*>(mine + S::QF + S::QZ + S::QH);  // [64] tiles j at j % 64
+  uint8_t* kept = reinterpret_cast<uint8_t*>(tiles + 64);               // [32] kept key rows of the issue's unit
+  uint8_t* kring = smem + S::RING + warp * S::WARP_RING;
+  uint8_t* vring = kring + SK * S::KPART;
+  for (int i = lane; i < (S::QF + S::QZ + S::QH) / 4; i += 32) qf[i] = 0;  // columns of absent heads stay zero
   if (lane == 0) {
-    for (int s = 0; s < ST; ++s) mbar_init(bars + 8 * s, 1);
+    // with a mask every lane copies key rows and arrives beside the bulk copy of the rest
+    for (int s = 0; s < kMaxSlots; ++s) {
+      mbar_init(kbars + 8 * s, a.mask ? 33 : 1);
+      mbar_init(vbars + 8 * s, 1);
+    }
     mbar_fence_init();
   }
   __syncthreads();
 
-  const int total = chunk[256] * c.H;
+  const int total = chunk[TH] * c.H;
   const int ranks = min(W * kSms, total);
   const int rank = warp * kSms + blockIdx.x;
   if (rank >= ranks) {
@@ -212,184 +283,247 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE>::WARPS * 32, 1) k_page
 
   // ---- one lane looks up one tile, 32 tiles at a time
   auto look_up = [&](int k) {
-    Tile d;
-    d.src = nullptr;
-    d.nval = 0;
-    d.unit = -1;
-    d.msk = 0;
     const int x = 32 * k + lane;
-    if (x >= n) return d;
-    const int ti = t0 + x;
-    int lo = 0, hi = 256;  // chunk[lo] * H <= ti < chunk[hi] * H
-    while (hi - lo > 1) {
-      const int m = (lo + hi) >> 1;
-      if (chunk[m] * c.H <= ti)
-        lo = m;
-      else
-        hi = m;
+    if (x < n) {
+      const int ti = t0 + x;
+      int lo = 0, hi = TH;  // chunk[lo] * H <= ti < chunk[hi] * H
+      while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (chunk[m] * c.H <= ti)
+          lo = m;
+        else
+          hi = m;
+      }
+      int b = lo * per_chunk, r = ti - chunk[lo] * c.H, tb = tiles_of(a, b);
+      while (r >= tb * c.H) {
+        r -= tb * c.H;
+        tb = tiles_of(a, ++b);
+      }
+      const int h = r / tb, pos = (r - h * tb) * kBlockTokens;
+      Tile d;
+      d.unit = b * c.H + h;
+      d.nval = min(min(max(a.lens[b], 0), a.max_len) - pos, kBlockTokens);
+      d.msk = a.mask ? a.mask[d.unit] : kFull;
+      const int pg = pos / c.page_tokens;
+      const int page = a.table[(size_t)b * a.max_pages + pg];
+      d.block = -1;
+      if (page >= 0 && page < c.num_pages) d.block = (page * c.H + h) * c.blocks + (pos - pg * c.page_tokens) / kBlockTokens;
+      if (d.block >= 0 && !kvq_in_bounds((size_t)d.block * c.block_bytes, c.block_bytes, c.pool_bytes())) d.block = -1;
+      if (d.block < 0) d.nval = 0;
+      tiles[x & 63] = d;
     }
-    int b = lo * per_chunk, r = ti - chunk[lo] * c.H, tb = tiles_of(a, b);
-    while (r >= tb * c.H) {
-      r -= tb * c.H;
-      tb = tiles_of(a, ++b);
-    }
-    const int h = r / tb, i = r - h * tb;
-    d.unit = b * c.H + h;
-    d.nval = min(min(max(a.lens[b], 0), a.max_len) - i * kBlockTokens, kBlockTokens);
-    d.msk = a.mask ? a.mask[d.unit] : kFull;
-    const int pos = i * kBlockTokens;
-    const int page = a.table[(size_t)b * a.max_pages + pos / c.page_tokens];
-    if (page >= 0 && page < c.num_pages) {
-      const size_t at = c.block_offset(page, h, pos % c.page_tokens);
-      if (kvq_in_bounds(at, lay.bytes, c.pool_bytes())) d.src = c.pages + at;
-    }
-    if (!d.src) d.nval = 0;
-    return d;
+    __syncwarp();
   };
-  Tile cur = look_up(0), nxt = look_up(1);
-  int batch = 0;  // index of cur's batch
+  look_up(0);
 
+  // ---- ring copies.  Without a mask a block's key part is one bulk copy.  With
+  // one, its kept rows are spread over the lanes in 16-byte pieces (a bulk copy
+  // per run of rows costs some 15 instructions each, issued one lane at a
+  // time); lane's q-th piece is piece 32 q + lane of the kept rows, and where
+  // the pieces are changes with the unit only.
   constexpr int KROW = kBlockTokens * KB / 2;  // bytes of a key row of 4 channels
-  auto issue = [&](int j) {
-    const Tile& d = (j >> 5) == batch ? cur : nxt;
-    const int from = j & 31;
-    const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(kFull, reinterpret_cast<uint64_t>(d.src), from));
-    const uint32_t msk = __shfl_sync(kFull, d.msk, from);
-    const int s = j % ST;
-    const uint32_t bar = bars + 8 * s, dst = smem_addr(ring + s * lay.bytes);
-    if (src == nullptr) {
-      if (lane == 0) mbar_arrive_expect_tx(bar, 0);
+  constexpr int PPR = KROW / 16, NPC = 32 * PPR / 32;  // pieces per row, and per lane
+  uint32_t run_msk = kFull;
+  int n_pieces = 32 * PPR;
+  int piece_at[NPC];
+#pragma unroll
+  for (int q = 0; q < NPC; ++q) piece_at[q] = (32 * q + lane) * 16;
+  auto issue_keys = [&](int j, int s) {
+    const Tile d = tiles[j & 63];
+    const uint32_t bar = kbars + 8 * s, dst = smem_addr(kring + s * S::KPART);
+    const uint8_t* src = c.pages + (size_t)d.block * c.block_bytes;
+    if (!a.mask) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, d.block >= 0 ? S::KPART : 0);
+        if (d.block >= 0) bulk_g2s(dst, src, S::KPART, bar);
+      }
       return;
     }
-    if (msk == kFull) {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar, lay.bytes);
-        bulk_g2s(dst, src, lay.bytes, bar);
-      }
-    } else {
-      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(msk) * KROW + lay.bytes - lay.ks);
+    if (d.msk != run_msk) {
+      run_msk = d.msk;
+      n_pieces = __popc(run_msk) * PPR;
+      if ((run_msk >> lane) & 1u) kept[__popc(run_msk & ((1u << lane) - 1u))] = (uint8_t)lane;
       __syncwarp();
-      if (((msk >> lane) & 1u) && (lane == 0 || !((msk >> (lane - 1)) & 1u))) {  // a run of kept rows starts here
-        const uint32_t rest = ~(msk >> lane);  // msk is not full, so a zero bit follows or the shift brought one
-        const int run = __ffs(rest) - 1;
-        bulk_g2s(dst + lane * KROW, src + lane * KROW, run * KROW, bar);
+#pragma unroll
+      for (int q = 0; q < NPC; ++q) {
+        const int pc = 32 * q + lane;
+        if (pc < n_pieces) piece_at[q] = kept[pc / PPR] * KROW + pc % PPR * 16;
       }
-      if (lane == 31) bulk_g2s(dst + lay.ks, src + lay.ks, lay.bytes - lay.ks, bar);
+      __syncwarp();
+    }
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, d.block >= 0 ? S::KPART - S::K_SCALES : 0);
+      if (d.block >= 0) bulk_g2s(dst + S::K_SCALES, src + S::K_SCALES, S::KPART - S::K_SCALES, bar);
+    }
+    if (d.block >= 0) {
+#pragma unroll
+      for (int q = 0; q < NPC; ++q)
+        if (32 * q + lane < n_pieces) copy16(dst + piece_at[q], src + piece_at[q]);
+    }
+    copies_arrive(bar);
+  };
+  auto issue_values = [&](int j, int s) {
+    if (lane == 0) {
+      const int block = tiles[j & 63].block;
+      mbar_arrive_expect_tx(vbars + 8 * s, block >= 0 ? S::VPART : 0);
+      if (block >= 0)
+        bulk_g2s(smem_addr(vring + s * S::VPART), c.pages + (size_t)block * c.block_bytes + S::KPART, S::VPART, vbars + 8 * s);
     }
   };
-  for (int j = 0; j < min(ST, n); ++j) issue(j);
+#pragma unroll 1
+  for (int j = 0; j < min(max(SK, SV), n); ++j) {
+    if (j < SK) issue_keys(j, j);
+    if (j < SV) issue_values(j, j);
+  }
 
-  bool ok = true;
   int unit = -1;
-  float M[HT], l[HT], zs[kGroups][HT], O[8][OC], fac[HT], q0[HT];
+  float M[HT], l[HT], O[8][OC], fac[HT], q0[HT];  // fac: score units to log2
+  // zero-point sums: per group and head of the thread's own tokens (fp32), or
+  // as the product with the zeros leaves them (rows: groups)
+  float zs[kGroups][HT], zp[NH][4];
+  float smax = 0.0f, plim = kTop16;  // largest value scale met, bound of p that keeps P' in fp16
 
   constexpr int kTop = PREC ? 6 : 14;
   constexpr float kCode = PREC ? 1.0f : 1.0f / 16777216.0f;  // what a code of 1 is to the matrix unit
 
-  // ---- a segment's query: rotated, masked, split into pieces, as fragments
+  // ---- a segment's query: rotated, masked, split into pieces, as fragments.
+  // Four heads at a time, eight lanes per head, a lane holding 16 channels: few
+  // shuffles and short chains, since no score can start before it is done.
   auto begin_segment = [&](int u, uint32_t msk) {
     const int b = u / c.H, h = u - b * c.H;
     __syncwarp();
-    for (int j = 0; j < a.G; ++j) {
-      const size_t at = (size_t)b * a.q_stride + ((size_t)h * a.G + j) * kHeadDim + 4 * lane;
-      float x[4];
-      if (a.dtype == KVQ_F32)
-        load4(static_cast<const float*>(a.q) + at, x);
-      else if (a.dtype == KVQ_BF16)
-        load4(static_cast<const __nv_bfloat16*>(a.q) + at, x);
-      else
-        load4(static_cast<const __half*>(a.q) + at, x);
-      if (c.rotate_k) {
-        float y0 = x[0] + x[1], y1 = x[0] - x[1], y2 = x[2] + x[3], y3 = x[2] - x[3];
-        x[0] = y0 + y2;
-        x[1] = y1 + y3;
-        x[2] = y0 - y2;
-        x[3] = y1 - y3;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-          const float sg = (lane & m) ? -1.0f : 1.0f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = fmaf(sg, x[i], __shfl_xor_sync(kFull, x[i], m));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] *= 0.08838834764831845f;  // 1 / sqrt(128)
-      }
-      const bool sel = (msk >> lane) & 1u;
-      float first = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = sel ? x[i] : 0.0f;
-      if (ch0) {
-        first = x[0];
-        if (lane == 0) x[0] = 0.0f;
-      }
-      // a power of two that takes the head's largest channel to [2^14, 2^15)
-      // (fp32 outputs, whose codes are not scaled by 2^-24: to [2^6, 2^7))
-      const float top = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
-      const int ex = top > 0.0f ? min(max(kTop - ilogbf(top), -100), 100) : 0;
-      const float up = ldexpf(1.0f, ex);
-      float sum = 0.0f;
+#pragma unroll 1
+    for (int j0 = 0; j0 < a.G; j0 += 4) {
+      const int j = j0 + (lane >> 3), part = lane & 7;  // channels 16 part .. 16 part + 15
+      const bool live = j < a.G;
+      const size_t at = (size_t)b * a.q_stride + ((size_t)h * a.G + (live ? j : 0)) * kHeadDim + 16 * part;
+      float x[16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        float f[4];
+        if (a.dtype == KVQ_F32)
+          load4(static_cast<const float*>(a.q) + at + 4 * i, f);
+        else if (a.dtype == KVQ_BF16)
+          load4(static_cast<const __nv_bfloat16*>(a.q) + at + 4 * i, f);
+        else
+          load4(static_cast<const __half*>(a.q) + at + 4 * i, f);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[4 * i + r] = f[r];
+      }
+      if (c.rotate_k) {
+#pragma unroll
+        for (int hs = 1; hs < 16; hs <<= 1)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if ((i & hs) == 0) {
+              const float y0 = x[i] + x[i + hs], y1 = x[i] - x[i + hs];
+              x[i] = y0;
+              x[i + hs] = y1;
+            }
+#pragma unroll
+        for (int m = 1; m < 8; m <<= 1) {
+          const float sg = (lane & m) ? -1.0f : 1.0f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = fmaf(sg, x[i], __shfl_xor_sync(kFull, x[i], m));
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] *= 0.08838834764831845f;  // 1 / sqrt(128)
+      }
+      float first = 0.0f, top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = ((msk >> (4 * part + (i >> 2))) & 1u) ? x[i] : 0.0f;
+      if (CH0) {
+        first = x[0];  // of part 0
+        if (part == 0) x[0] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
+      // a power of two that takes the head's largest channel to [2^14, 2^15)
+      // (fp32 outputs, whose codes are not scaled by 2^-24: to [2^6, 2^7))
+#pragma unroll
+      for (int m = 1; m < 8; m <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, m));
+      const int ex = min(max(kTop + 127 - (__float_as_int(top) >> 23), -100), 100);
+      const float up = __int_as_float((127 + ex) << 23);
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
         x[i] *= up;
         sum += x[i];
       }
-      // K-steps and columns of this lane's four channels
+      sum += __shfl_xor_sync(kFull, sum, 1);  // two lanes hold a quantization group
+      // K-steps and columns of this lane's four channel groups p = 4 part + i
       const int nt_hi = HC == 16 ? j >> 3 : 0, nt_lo = HC == 4 ? 0 : HC == 8 ? 1 : 2 + (j >> 3);
       const int n_hi = HC == 4 ? 2 * j : j & 7, n_lo = HC == 4 ? 2 * j + 1 : j & 7;
-      if (KB == 4) {
-        const float y[4] = {x[0], x[2], x[1] * (1.0f / 16.0f), x[3] * (1.0f / 16.0f)};
-        float e[4];
-        __half hh[4];
+      if (live) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          hh[i] = __float2half_rn(y[i]);
-          e[i] = (y[i] - __half2float(hh[i])) * 2048.0f;
+          float y[4], e[4];
+          if (KB == 4) {  // (channels 0, 2), (1, 3) / 16, minus what a whole byte brings of the upper field
+            y[0] = x[4 * i];
+            y[1] = x[4 * i + 2];
+            y[2] = x[4 * i + 1] * (1.0f / 16.0f) - (PREC ? 0.0f : y[0]);
+            y[3] = x[4 * i + 3] * (1.0f / 16.0f) - (PREC ? 0.0f : y[1]);
+          } else {
+            y[0] = x[4 * i];
+            y[1] = x[4 * i + 1] * 0.25f;
+            y[2] = x[4 * i + 2] * 0.0625f;
+            y[3] = x[4 * i + 3] * 0.015625f;
+          }
+          const uint32_t h01 = half2_of(y[0], y[1]), h23 = half2_of(y[2], y[3]);
+          const float2 f01 = float2_of(h01), f23 = float2_of(h23);
+          e[0] = (y[0] - f01.x) * 2048.0f;
+          e[1] = (y[1] - f01.y) * 2048.0f;
+          e[2] = (y[2] - f23.x) * 2048.0f;
+          e[3] = (y[3] - f23.y) * 2048.0f;
+          const uint32_t l01 = half2_of(e[0], e[1]), l23 = half2_of(e[2], e[3]);
+          if (KB == 4) {  // step part, column i
+            reinterpret_cast<uint2*>(qf)[(part * NT + nt_hi) * 32 + n_hi * 4 + i] = make_uint2(h01, h23);
+            reinterpret_cast<uint2*>(qf)[(part * NT + nt_lo) * 32 + n_lo * 4 + i] = make_uint2(l01, l23);
+          } else {  // steps 2 Q (channels 0, 1) and 2 Q + 1 (channels 2, 3), column i; the side of the pair by the lane
+            uint16_t* q16 = reinterpret_cast<uint16_t*>(qf) + (part & 1);
+            const int Q = part >> 1;
+            const int hi = ((2 * Q * NT + nt_hi) * 32 + n_hi * 4 + i) * 4, lo = ((2 * Q * NT + nt_lo) * 32 + n_lo * 4 + i) * 4;
+            constexpr int next = NT * 32 * 4;
+            q16[hi] = (uint16_t)h01;
+            q16[hi + 2] = (uint16_t)(h01 >> 16);
+            q16[hi + next] = (uint16_t)h23;
+            q16[hi + next + 2] = (uint16_t)(h23 >> 16);
+            q16[lo] = (uint16_t)l01;
+            q16[lo + 2] = (uint16_t)(l01 >> 16);
+            q16[lo + next] = (uint16_t)l23;
+            q16[lo + next + 2] = (uint16_t)(l23 >> 16);
+          }
         }
-        const int step = lane >> 2, col = lane & 3;
-        uint2 v;
-        v.x = half2_of(__half2float(hh[0]), __half2float(hh[1]));
-        v.y = half2_of(__half2float(hh[2]), __half2float(hh[3]));
-        reinterpret_cast<uint2*>(qf)[(step * NT + nt_hi) * 32 + n_hi * 4 + col] = v;
-        v.x = half2_of(e[0], e[1]);
-        v.y = half2_of(e[2], e[3]);
-        reinterpret_cast<uint2*>(qf)[(step * NT + nt_lo) * 32 + n_lo * 4 + col] = v;
-      } else {
-        const int Q = lane >> 3, col = lane & 3, side = (lane >> 2) & 1;
-        __half* qfh = reinterpret_cast<__half*>(qf);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float y = x[i] * (i == 0 ? 1.0f : i == 1 ? 0.25f : i == 2 ? 0.0625f : 0.015625f);
+        if ((part & 1) == 0) {  // group part / 2: K positions 2 c + b of the zero-point product
+          const int Q = part >> 1;
+          const float y = sum * kCode;
           const __half hi = __float2half_rn(y);
-          const int step = 2 * Q + (i >> 1);
-          qfh[(((step * NT + nt_hi) * 32 + n_hi * 4 + col) * 2 + (i & 1)) * 2 + side] = hi;
-          qfh[(((step * NT + nt_lo) * 32 + n_lo * 4 + col) * 2 + (i & 1)) * 2 + side] =
-              __float2half_rn((y - __half2float(hi)) * 2048.0f);
+          __half* z = reinterpret_cast<__half*>(qz);
+          z[(nt_hi * 32 + n_hi * 4 + (Q >> 1)) * 2 + (Q & 1)] = hi;
+          z[(nt_lo * 32 + n_lo * 4 + (Q >> 1)) * 2 + (Q & 1)] = __float2half_rn((y - __half2float(hi)) * 2048.0f);
         }
+        if (part == 0)
+          qh[j] = make_float2(a.scale_log2 * __int_as_float((127 + (PREC ? 0 : 24) - ex) << 23), first * up * kCode);
       }
-#pragma unroll
-      for (int m = 1; m < 8; m <<= 1) sum += __shfl_xor_sync(kFull, sum, m);
-      if ((lane & 7) == 0) {  // group lane / 8: K positions 2 c + b of the zero-point product
-        const int Q = lane >> 3;
-        const float y = sum * kCode;
-        const __half hi = __float2half_rn(y);
-        __half* z = reinterpret_cast<__half*>(qz);
-        z[(nt_hi * 32 + n_hi * 4 + (Q >> 1)) * 2 + (Q & 1)] = hi;
-        z[(nt_lo * 32 + n_lo * 4 + (Q >> 1)) * 2 + (Q & 1)] = __float2half_rn((y - __half2float(hi)) * 2048.0f);
-      }
-      if (lane == 0) qh[j] = make_float2(a.scale_log2 * ldexpf(1.0f, (PREC ? 0 : 24) - ex), first * up * kCode);
     }
     __syncwarp();
+    smax = 0.0f;
+    plim = kTop16;
 #pragma unroll
     for (int k = 0; k < HT; ++k) {
       const int hd = HC == 4 ? cq : 8 * (k >> 1) + 2 * cq + (k & 1);
       const float2 v = qh[hd];
-      fac[k] = v.x;
+      fac[k] = v.x == 0.0f ? 1.0e-37f : v.x;  // a scale of 0 still tells masked tokens (-inf) from the others
       q0[k] = v.y;
       M[k] = kMStart;
       l[k] = 0.0f;
 #pragma unroll
       for (int r = 0; r < kGroups; ++r) zs[r][k] = 0.0f;
     }
+#pragma unroll
+    for (int t = 0; t < NH; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) zp[t][r] = 0.0f;
 #pragma unroll
     for (int m = 0; m < 8; ++m)
 #pragma unroll
@@ -403,11 +537,17 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE>::WARPS * 32, 1) k_page
 #pragma unroll
       for (int m = 4; m < 32; m <<= 1) {
         l[k] += __shfl_xor_sync(kFull, l[k], m);
+        if (PREC) {
 #pragma unroll
-        for (int r = 0; r < kGroups; ++r) zs[r][k] += __shfl_xor_sync(kFull, zs[r][k], m);
+          for (int r = 0; r < kGroups; ++r) zs[r][k] += __shfl_xor_sync(kFull, zs[r][k], m);
+        }
+      }
+      if (!PREC) {  // group r: row r (even tokens) and row 12 + r (odd ones) of the zeros' product
+#pragma unroll
+        for (int r = 0; r < kGroups; ++r)
+          zs[r][k] = __shfl_sync(kFull, zp[k >> 1][k & 1], 4 * r + cq) + __shfl_sync(kFull, zp[k >> 1][2 + (k & 1)], 16 + 4 * r + cq);
       }
     }
-    const float nan = __int_as_float(0x7fc00000);
     constexpr float kOne = 1.0f / kCode;
 #pragma unroll
     for (int k = 0; k < HT; ++k) {
@@ -415,7 +555,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE>::WARPS * 32, 1) k_page
       if (hd >= a.G) continue;
       const size_t row = (size_t)(unit + rank) * a.G + hd;
       if (!kvq_in_bounds(row, 1, a.part_rows)) continue;
-      if (g == 0) a.part_ml[row] = ok ? make_float2(M[k], l[k]) : make_float2(nan, nan);
+      if (g == 0) a.part_ml[row] = make_float2(M[k], l[k]);
       float* dst = a.part_acc + row * kHeadDim;
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
@@ -434,45 +574,39 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE>::WARPS * 32, 1) k_page
     }
   };
 
-  int s = 0, phase = 0;
-  for (int j = 0; j < n; ++j) {
-    if ((j >> 5) != batch) {
-      ++batch;
-      cur = nxt;
-      nxt = look_up(batch + 1);
+  int sk = 0, sv = 0, pk = 0, pv = 0;  // ring slots and their phases
+  int j = 0;
+#pragma unroll 1
+  for (; j < n; ++j) {
+    if ((j & 31) == 0) look_up((j >> 5) + 1);  // the issue runs at most 4 tiles ahead
+    const Tile now = tiles[j & 63];
+    const int nval = now.nval;
+    if (now.unit != unit) {
+      unit = now.unit;
+      begin_segment(unit, now.msk);
     }
-    const int from = j & 31;
-    const int u = __shfl_sync(kFull, cur.unit, from);
-    const int nval = __shfl_sync(kFull, cur.nval, from);
-    if (u != unit) {
-      if (unit >= 0) end_segment();
-      unit = u;
-      begin_segment(u, __shfl_sync(kFull, cur.msk, from));
-    }
-    if (ok) ok = wait_full(bars + 8 * s, phase);
-    ok = __all_sync(kFull, ok);
-    if (nval > 0 && ok) {
-      const uint8_t* st = ring + s * lay.bytes;
+    if (!wait_full(kbars + 8 * sk, pk)) break;
+    float p[4][2][HT];  // the scores, then 2^(score - M), of tokens 8g + 2i + e
+    if (nval > 0) {
+      const uint8_t* st = kring + sk * S::KPART;
       // ================================================================ scores
       float acc[4][NT][4];
       {
-        const uint4 z0 = *reinterpret_cast<const uint4*>(st + lay.kz + (g * 2 + (cq & 1)) * 16);
-        const uint4 z1 = *reinterpret_cast<const uint4*>(st + lay.kz + ((8 + g) * 2 + (cq & 1)) * 16);
+        const uint4 z0 = *reinterpret_cast<const uint4*>(st + S::K_ZEROS + (g * 2 + (cq & 1)) * 16);
+        const uint4 z1 = *reinterpret_cast<const uint4*>(st + S::K_ZEROS + ((8 + g) * 2 + (cq & 1)) * 16);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint32_t bz = qz[nt * 32 + lane];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][nt][r] = 0.0f;
             const uint4& z = i < 2 ? z0 : z1;
-            mma8(acc[i][nt], (i & 1) ? z.z : z.x, (i & 1) ? z.w : z.y, bz);
+            mma8z(acc[i][nt], (i & 1) ? z.z : z.x, (i & 1) ? z.w : z.y, bz);
           }
         }
       }
       uint4 ks[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ks[i] = *reinterpret_cast<const uint4*>(st + lay.ks + 16 * (8 * i + g));
+      for (int i = 0; i < 4; ++i) ks[i] = *reinterpret_cast<const uint4*>(st + S::K_SCALES + 16 * (8 * i + g));
 #pragma unroll
       for (int Q = 0; Q < kGroups; ++Q) {
         uint2 bA[NT], bB[NT];
@@ -495,19 +629,38 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE>::WARPS * 32, 1) k_page
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t x = word(w0, i), y = KB == 4 ? word(w1, i) : x;
-          const uint32_t xs = x >> 8, ys = KB == 4 ? y >> 8 : xs;
-          constexpr uint32_t m0 = KB == 4 ? 0x000F000Fu : 0x00030003u, m1 = KB == 4 ? 0x00F000F0u : 0x000C000Cu;
-          constexpr uint32_t m2 = KB == 4 ? m0 : 0x00300030u, m3 = KB == 4 ? m1 : 0x00C000C0u;
-          const uint32_t ka[8] = {codes_of<PREC>(x, m0, 0), codes_of<PREC>(xs, m0, 0), codes_of<PREC>(x, m1, 0),
-                                  codes_of<PREC>(xs, m1, 0), codes_of<PREC>(y, m2, 0), codes_of<PREC>(ys, m2, 0),
-                                  codes_of<PREC>(y, m3, 0), codes_of<PREC>(ys, m3, 0)};
+          uint32_t ka[8];
+          if (KB == 4 && !PREC) {
+            // a token's byte whole (code + 16 code'), and its upper field: the query is
+            // given in that basis
+            ka[0] = __byte_perm(word(w0, i), 0, 0x4240);
+            ka[1] = __byte_perm(word(w0, i), 0, 0x4341);
+            ka[2] = ka[0] & 0x00F000F0u;
+            ka[3] = ka[1] & 0x00F000F0u;
+            ka[4] = __byte_perm(word(w1, i), 0, 0x4240);
+            ka[5] = __byte_perm(word(w1, i), 0, 0x4341);
+            ka[6] = ka[4] & 0x00F000F0u;
+            ka[7] = ka[5] & 0x00F000F0u;
+          } else {
+            const uint32_t x = word(w0, i), y = KB == 4 ? word(w1, i) : x;
+            const uint32_t xs = x >> 8, ys = KB == 4 ? y >> 8 : xs;
+            constexpr uint32_t m0 = KB == 4 ? 0x000F000Fu : 0x00030003u, m1 = KB == 4 ? 0x00F000F0u : 0x000C000Cu;
+            constexpr uint32_t m2 = KB == 4 ? m0 : 0x00300030u, m3 = KB == 4 ? m1 : 0x00C000C0u;
+            ka[0] = codes_of<PREC>(x, m0, 0);
+            ka[1] = codes_of<PREC>(xs, m0, 0);
+            ka[2] = codes_of<PREC>(x, m1, 0);
+            ka[3] = codes_of<PREC>(xs, m1, 0);
+            ka[4] = codes_of<PREC>(y, m2, 0);
+            ka[5] = codes_of<PREC>(ys, m2, 0);
+            ka[6] = codes_of<PREC>(y, m3, 0);
+            ka[7] = codes_of<PREC>(ys, m3, 0);
+          }
           const float2 sa = float2_of((Q >> 1) ? ks[i].y : ks[i].x), sb = float2_of((Q >> 1) ? ks[i].w : ks[i].z);
           const float s0 = (Q & 1) ? sa.y : sa.x, s1 = (Q & 1) ? sb.y : sb.x;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma16(d, ka[0], ka[1], ka[2], ka[3], bA[nt].x, bA[nt].y);
+            float d[4];
+            mma16z(d, ka[0], ka[1], ka[2], ka[3], bA[nt].x, bA[nt].y);
             mma16(d, ka[4], ka[5], ka[6], ka[7], bB[nt].x, bB[nt].y);
             acc[i][nt][0] = fmaf(s0, d[0], acc[i][nt][0]);
             acc[i][nt][1] = fmaf(s0, d[1], acc[i][nt][1]);
@@ -516,130 +669,177 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE>::WARPS * 32, 1) k_page
           }
         }
       }
-      // log2-domain scores of this lane's tokens 8g + 2i + e and heads
-      float p[4][2][HT];
-      {
-        uint4 k0 = make_uint4(0, 0, 0, 0);
-        if (ch0) k0 = *reinterpret_cast<const uint4*>(st + lay.k0 + 16 * g);
+      uint4 k0 = make_uint4(0, 0, 0, 0);
+      if (CH0) k0 = *reinterpret_cast<const uint4*>(st + S::K_CH0 + 16 * g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t kk = word(k0, i);
-            const float kv = __uint_as_float(e ? kk & 0xFFFF0000u : kk << 16);
-            const bool valid = 8 * g + 2 * i + e < nval;
-#pragma unroll
-            for (int k = 0; k < HT; ++k) {
-              float hi, lo;
-              if (HC == 4) {
-                hi = acc[i][0][2 * e];
-                lo = acc[i][0][2 * e + 1];
-              } else {
-                hi = acc[i][k >> 1][2 * e + (k & 1)];
-                lo = acc[i][NT / 2 + (k >> 1)][2 * e + (k & 1)];
-              }
-              float sc = fmaf(lo, kLow, hi);
-              if (ch0) sc = fmaf(q0[k], kv, sc);
-              p[i][e][k] = valid ? sc * fac[k] : -INFINITY;
-            }
-          }
-      }
-      // ================================================================ softmax
-      uint4 vs[4];
-      float smax[4][2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        vs[i] = *reinterpret_cast<const uint4*>(st + lay.vs + 16 * (8 * i + g));
-        if (nval < kBlockTokens) {  // bytes behind the last token may hold anything
-          if (8 * g + 2 * i >= nval) vs[i].x = vs[i].y = 0;
-          if (8 * g + 2 * i + 1 >= nval) vs[i].z = vs[i].w = 0;
-        }
-        const __half2 ma = __hmax2(*reinterpret_cast<__half2*>(&vs[i].x), *reinterpret_cast<__half2*>(&vs[i].y));
-        const __half2 mb = __hmax2(*reinterpret_cast<__half2*>(&vs[i].z), *reinterpret_cast<__half2*>(&vs[i].w));
-        constexpr float kTiny = 1.0f / 16777216.0f;  // the smallest fp16 scale: bounds p where a scale is 0
-        smax[i][0] = fmaxf(__half2float(__hmax(__low2half(ma), __high2half(ma))), kTiny);
-        smax[i][1] = fmaxf(__half2float(__hmax(__low2half(mb), __high2half(mb))), kTiny);
-      }
-      {
-        // p = 2^(s - M); M rises when some p * scale would pass 2^15
-        bool over = false;
-        float x[4][2][HT];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int k = 0; k < HT; ++k) {
-              x[i][e][k] = ex2(p[i][e][k] - M[k]);
-              over |= x[i][e][k] * smax[i][e] > 32768.0f;
-            }
-        if (__any_sync(kFull, over)) {
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t kk = word(k0, i);
+          const float kv = __uint_as_float(e ? kk & 0xFFFF0000u : kk << 16);
 #pragma unroll
           for (int k = 0; k < HT; ++k) {
-            float t = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) t = fmaxf(t, p[i][e][k] + __log2f(smax[i][e]));
-#pragma unroll
-            for (int m = 4; m < 32; m <<= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, m));
-            const float m_new = fmaxf(M[k], t - 7.0f);  // the largest P' becomes 2^7: room for 2^8 more
-            const float al = ex2(M[k] - m_new);
-            M[k] = m_new;
-            l[k] *= al;
-#pragma unroll
-            for (int r = 0; r < kGroups; ++r) zs[r][k] *= al;
-#pragma unroll
-            for (int m = 0; m < 8; ++m) {
-              if (HC == 4) {
-                O[m][0] *= al;
-                O[m][1] *= al;
-              } else {
-                O[m][4 * (k >> 1) + (k & 1)] *= al;
-                O[m][4 * (k >> 1) + 2 + (k & 1)] *= al;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) x[i][e][k] = ex2(p[i][e][k] - m_new);
+            const float hi = HC == 4 ? acc[i][0][2 * e] : acc[i][k >> 1][2 * e + (k & 1)];
+            const float lo = HC == 4 ? acc[i][0][2 * e + 1] : acc[i][NT / 2 + (k >> 1)][2 * e + (k & 1)];
+            float sc = fmaf(lo, kLow, hi);
+            if (CH0) sc = fmaf(q0[k], kv, sc);
+            p[i][e][k] = sc;
           }
         }
+      if (nval < kBlockTokens) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int k = 0; k < HT; ++k) {
-              p[i][e][k] = x[i][e][k];
-              l[k] += x[i][e][k];
-            }
+            for (int k = 0; k < HT; ++k)
+              if (8 * g + 2 * i + e >= nval) p[i][e][k] = fac[k] < 0.0f ? INFINITY : -INFINITY;
       }
-      // zero-point terms sum_t p z, per group (codes counted from their middle: z + middle * scale)
-      constexpr int kMid = VB == 4 ? 8 : 2;
+    }
+    __syncwarp();  // every lane has read the slot
+    if (j + SK < n) issue_keys(j + SK, sk);
+    if (++sk == SK) {
+      sk = 0;
+      pk ^= 1;
+    }
+    if (!wait_full(vbars + 8 * sv, pv)) break;
+    if (nval > 0) {
+      uint8_t* st = vring + sv * S::VPART;
+      if (nval < kBlockTokens) {  // bytes behind the last token may hold anything: no scale, no zero there
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint4 vz = *reinterpret_cast<const uint4*>(st + lay.vz + 16 * (8 * i + g));
-        if (nval < kBlockTokens) {
-          if (8 * g + 2 * i >= nval) vz.x = vz.y = 0;
-          if (8 * g + 2 * i + 1 >= nval) vz.z = vz.w = 0;
+        for (int t = lane; t < kBlockTokens; t += 32)
+          if (t >= nval) {
+            *reinterpret_cast<uint2*>(st + S::V_SCALES + 2 * scale_index(t, 0)) = make_uint2(0, 0);
+            *reinterpret_cast<uint2*>(st + S::V_ZEROS + 2 * scale_index(t, 0)) = make_uint2(0, 0);
+          }
+        fence_proxy_async();  // before a later copy into this slot
+        __syncwarp();
+      }
+      uint4 vs[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) vs[i] = *reinterpret_cast<const uint4*>(st + S::V_SCALES + 16 * (8 * i + g));
+      // ================================================================ softmax
+      // p = 2^(s - M) against bounds: p <= plim keeps p and p * scale below 2^15.
+      // Lane (g, cq) checks the scales of two of its row's tokens.
+      float tile_scale;
+      {
+        const uint4 v = *reinterpret_cast<const uint4*>(st + S::V_SCALES + 16 * (8 * cq + g));
+        const float2 m = float2_of(hmax2(hmax2(v.x, v.y), hmax2(v.z, v.w)));
+        tile_scale = fmaxf(m.x, m.y);
+      }
+      bool over = tile_scale > smax;
+      float x[4][2][HT];
+#pragma unroll
+      for (int k = 0; k < HT; ++k) {
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i][0][k] = ex2(fmaf(p[i][0][k], fac[k], -M[k]));
+          x[i][1][k] = ex2(fmaf(p[i][1][k], fac[k], -M[k]));
+          top = fmaxf(top, fmaxf(x[i][0][k], x[i][1][k]));
         }
+        over |= top > plim;
+      }
+      if (__any_sync(kFull, over)) {
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) tile_scale = fmaxf(tile_scale, __shfl_xor_sync(kFull, tile_scale, m));
+        if (tile_scale > smax) smax = 1.25f * tile_scale;  // the next largest ones do not come back here
+        plim = kTop16 / fmaxf(smax, 1.0f);
+        const float room = __log2f(plim) - 8.0f;  // the largest p becomes plim / 2^8
+#pragma unroll
+        for (int k = 0; k < HT; ++k) {
+          float t = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t = fmaxf(t, fmaxf(p[i][0][k] * fac[k], p[i][1][k] * fac[k]));
+#pragma unroll
+          for (int m = 4; m < 32; m <<= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, m));
+          const float m_new = fmaxf(M[k], t - room);
+          const float al = ex2(M[k] - m_new);
+          M[k] = m_new;
+          l[k] *= al;
+          if (PREC) {
+#pragma unroll
+            for (int r = 0; r < kGroups; ++r) zs[r][k] *= al;
+          } else {
+            zp[k >> 1][k & 1] *= al;
+            zp[k >> 1][2 + (k & 1)] *= al;
+          }
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            if (HC == 4) {
+              O[m][0] *= al;
+              O[m][1] *= al;
+            } else {
+              O[m][4 * (k >> 1) + (k & 1)] *= al;
+              O[m][4 * (k >> 1) + 2 + (k & 1)] *= al;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x[i][e][k] = ex2(fmaf(p[i][e][k], fac[k], -m_new));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float2 z = float2_of(word(vz, 2 * e + r));
-            if (MODE != kBf16) {
-              const float2 sv = float2_of(word(vs[i], 2 * e + r));
-              z.x = fmaf((float)kMid, sv.x, z.x);
-              z.y = fmaf((float)kMid, sv.y, z.y);
-            }
-#pragma unroll
-            for (int k = 0; k < HT; ++k) {
-              zs[2 * r][k] = fmaf(p[i][e][k], z.x, zs[2 * r][k]);
-              zs[2 * r + 1][k] = fmaf(p[i][e][k], z.y, zs[2 * r + 1][k]);
-            }
+          for (int k = 0; k < HT; ++k) {
+            p[i][e][k] = x[i][e][k];
+            l[k] += x[i][e][k];
           }
+      constexpr int kMid = VB == 4 ? 8 : 2;
+      uint32_t ph[4][2][NH];  // p as fp16: the head twice (HC = 4), or a pair of heads
+      if (!PREC) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int t = 0; t < NH; ++t)
+              ph[i][e][t] = HC == 4 ? half2_of(p[i][e][0], p[i][e][0]) : half2_of(p[i][e][(2 * t) % HT], p[i][e][(2 * t + 1) % HT]);
+        // zero-point sums: matrix i's transposed rows are (e, group), its columns the
+        // tokens 8u + 2i + e; rows 0-3 meet the even tokens in the lower half of K,
+        // rows 12-15 the odd ones in the upper half, the others are not used
+        uint4 z = load_transposed(smem_addr(st + S::V_ZEROS + 16 * lane));
+        if (MODE == kF16) {  // codes are counted from their middle: z + middle * scale
+          const uint4 zs4 = load_transposed(smem_addr(st + S::V_SCALES + 16 * lane));
+          const __half2 mid = __float2half2_rn((float)kMid);
+          uint32_t* zw = &z.x;
+          const uint32_t* sw = &zs4.x;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __half2 r = __hfma2(mid, *reinterpret_cast<const __half2*>(&sw[i]), *reinterpret_cast<const __half2*>(&zw[i]));
+            zw[i] = *reinterpret_cast<const uint32_t*>(&r);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < NH; ++t) {
+          float d[4];
+          mma16z(d, z.x, 0u, 0u, z.x, transpose8(ph[0][0][t]), transpose8(ph[0][1][t]));
+#pragma unroll
+          for (int i = 1; i < 4; ++i) mma16(d, word(z, i), 0u, 0u, word(z, i), transpose8(ph[i][0][t]), transpose8(ph[i][1][t]));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) zp[t][r] += d[r];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 vz = *reinterpret_cast<const uint4*>(st + S::V_ZEROS + 16 * (8 * i + g));
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float2 z = float2_of(word(vz, 2 * e + r)), sv = float2_of(word(vs[i], 2 * e + r));
+              const float za = fmaf((float)kMid, sv.x, z.x), zb = fmaf((float)kMid, sv.y, z.y);
+#pragma unroll
+              for (int k = 0; k < HT; ++k) {
+                zs[2 * r][k] = fmaf(p[i][e][k], za, zs[2 * r][k]);
+                zs[2 * r + 1][k] = fmaf(p[i][e][k], zb, zs[2 * r + 1][k]);
+              }
+            }
+        }
       }
       // ================================================================ value sums
       constexpr int NR = S::PAIR ? 2 : 4;  // rounds: a pair of groups or one group each
@@ -651,8 +851,11 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE>::WARPS * 32, 1) k_page
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             if (S::PAIR) {
-              const float2 sv = float2_of(word(vs[i], 2 * e + rd));
-              b[i][0][e] = transpose8(half2_of(p[i][e][0] * sv.x, p[i][e][0] * sv.y));
+              b[i][0][e] = transpose8(hmul2(ph[i][e][0], word(vs[i], 2 * e + rd)));
+            } else if (!PREC) {
+              const uint32_t sv = dup_half(word(vs[i], 2 * e + (rd >> 1)), rd & 1);
+#pragma unroll
+              for (int t = 0; t < NH; ++t) b[i][t][e] = transpose8(hmul2(ph[i][e][t], sv));
             } else {
               const float2 s2 = float2_of(word(vs[i], 2 * e + (rd >> 1)));
               const float sv = (rd & 1) ? s2.y : s2.x;
@@ -662,43 +865,41 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE>::WARPS * 32, 1) k_page
                 b[i][0][e] = transpose8(half2_of(hi, (v - hi) * 2048.0f));
               } else {
 #pragma unroll
-                for (int k = 0; k < HT; k += 2) {
-                  const float v0 = p[i][e][k] * sv, v1 = p[i][e][k + 1] * sv;
+                for (int t = 0; t < NH; ++t) {
+                  const float v0 = p[i][e][(2 * t) % HT] * sv, v1 = p[i][e][(2 * t + 1) % HT] * sv;
                   const uint32_t hi = half2_of(v0, v1);
-                  b[i][k >> 1][e] = transpose8(hi);
-                  if (PREC) {
-                    const float2 f = float2_of(hi);
-                    b[i][NP / 2 + (k >> 1)][e] = transpose8(half2_of((v0 - f.x) * 2048.0f, (v1 - f.y) * 2048.0f));
-                  }
+                  const float2 f = float2_of(hi);
+                  b[i][t][e] = transpose8(hi);
+                  b[i][(NP / 2 + t) % NP][e] = transpose8(half2_of((v0 - f.x) * 2048.0f, (v1 - f.y) * 2048.0f));
                 }
               }
             }
           }
         // minus the codes' middle times the sum of the rounded P' (all rows alike)
-        float base[NP][4] = {};
+        float base[NP][4];
         if (MODE == kF16) {
           constexpr uint32_t c0 = VB == 4 ? 0x80088008u : 0x80028002u, c1 = VB == 4 ? 0x80808080u : 0x80088008u;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int np = 0; np < NP; ++np) {
+            mma16z(base[np], c0, c1, c0, c1, b[0][np][0], b[0][np][1]);
 #pragma unroll
-            for (int np = 0; np < NP; ++np) mma16(base[np], c0, c1, c0, c1, b[i][np][0], b[i][np][1]);
+            for (int i = 1; i < 4; ++i) mma16(base[np], c0, c1, c0, c1, b[i][np][0], b[i][np][1]);
+          }
         }
         constexpr int MT = S::PAIR ? 4 : 2;  // 16-channel tiles of this round
 #pragma unroll
         for (int mm = 0; mm < MT; ++mm) {
           const int m = rd * MT + mm;
-          uint4 w;
-          if (VB == 4)
-            w = *reinterpret_cast<const uint4*>(st + lay.vc + (m * 8 + g) * 64 + cq * 16);
-          else
-            w = *reinterpret_cast<const uint4*>(st + lay.vc + ((m >> 1) * 8 + g) * 64 + cq * 16);
-          float d[NP][4];
-#pragma unroll
-          for (int np = 0; np < NP; ++np)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) d[np][r] = (VB == 2 && (m & 1)) ? 16.0f * base[np][r] : base[np][r];
+          const uint4 w = *reinterpret_cast<const uint4*>(st + ((VB == 4 ? m : m >> 1) * 8 + g) * 64 + cq * 16);
           const uint32_t m0 = VB == 4 ? 0x000F000Fu : (m & 1) ? 0x00300030u : 0x00030003u;
           const uint32_t m1 = VB == 4 ? 0x00F000F0u : (m & 1) ? 0x00C000C0u : 0x000C000Cu;
+          float d[NP][4];
+          if (MODE == kF16) {
+#pragma unroll
+            for (int np = 0; np < NP; ++np)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) d[np][r] = (VB == 2 && (m & 1)) ? 16.0f * base[np][r] : base[np][r];
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t x = word(w, i), xs = x >> 8;
@@ -707,7 +908,12 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE>::WARPS * 32, 1) k_page
             const uint32_t a0 = codes_of<PREC>(x, m0, f * kMid), a1 = codes_of<PREC>(x, m1, f * f1 * kMid);
             const uint32_t a2 = codes_of<PREC>(xs, m0, f * kMid), a3 = codes_of<PREC>(xs, m1, f * f1 * kMid);
 #pragma unroll
-            for (int np = 0; np < NP; ++np) mma16(d[np], a0, a1, a2, a3, b[i][np][0], b[i][np][1]);
+            for (int np = 0; np < NP; ++np) {
+              if (i == 0 && MODE != kF16)
+                mma16z(d[np], a0, a1, a2, a3, b[i][np][0], b[i][np][1]);
+              else
+                mma16(d[np], a0, a1, a2, a3, b[i][np][0], b[i][np][1]);
+            }
           }
           if (S::PAIR) {  // columns of this tile's group of the pair
             const int odd = (m >> 1) & 1;
@@ -718,42 +924,68 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE>::WARPS * 32, 1) k_page
             O[m][1] += fmaf(d[0][3], kLow, d[0][2]);
           } else {
 #pragma unroll
-            for (int t = 0; t < HC / 8; ++t)
+            for (int t = 0; t < NH; ++t)
 #pragma unroll
               for (int r = 0; r < 4; ++r)
-                O[m][4 * t + r] += PREC ? fmaf(d[NP / 2 + t][r], kLow, d[t][r]) : d[t][r];
+                O[m][4 * t + r] += PREC ? fmaf(d[(NP / 2 + t) % NP][r], kLow, d[t][r]) : d[t][r];
           }
         }
       }
     }
-    __syncwarp();  // every lane has read the stage
-    if (j + ST < n && ok) issue(j + ST);
-    if (++s == ST) {
-      s = 0;
-      phase ^= 1;
+    __syncwarp();  // every lane has read the slot
+    if (j + SV < n) issue_values(j + SV, sv);
+    if (++sv == SV) {
+      sv = 0;
+      pv ^= 1;
     }
+    if (j + 1 == n || tiles[(j + 1) & 63].unit != unit) end_segment();
   }
-  end_segment();
+  if (__builtin_expect(j < n, 0)) {
+    // a copy did not land in time: not-a-number partials for this segment and the
+    // rest of the range, and time for copies in flight to land before the
+    // shared memory is given up
+    int last = -1;
+    for (int x = j; x < n; ++x) {
+      if (x != j && (x & 31) == 0) look_up((x >> 5) + 1);
+      const int u = tiles[x & 63].unit;
+      if (u == last) continue;
+      last = u;
+      const size_t row = (size_t)(u + rank) * a.G + lane;
+      if (lane < a.G && kvq_in_bounds(row, 1, a.part_rows)) a.part_ml[row] = make_float2(NAN, NAN);
+    }
+    __nanosleep(64000);
+  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (lane == 0) a.status[rank] = ok ? 0 : 1;
-  if (!ok) __nanosleep(64000);  // copies still in flight land before the shared memory is given up
+  if (lane == 0) a.status[rank] = j < n;
+}
+
+template <int KB, int VB, int HC, int MODE, bool CH0>
+cudaError_t launch_one(const PagedDecodeArgs& a, cudaStream_t s) {
+  using S = Shape<KB, VB, HC, MODE, CH0>;
+  auto kern = k_paged_decode<KB, VB, HC, MODE, CH0>;
+  static std::atomic<uint64_t> ready{0};  // devices on which the kernel may take this much shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev > 63 || !(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev <= 63) ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  kern<<<kSms, S::THREADS, S::SMEM, s>>>(a);
+  return cudaGetLastError();
 }
 
 template <int KB, int VB, int HC, int MODE>
-cudaError_t launch_one(const PagedDecodeArgs& a, cudaStream_t s) {
-  using S = Shape<KB, VB, HC, MODE>;
-  auto kern = k_paged_decode<KB, VB, HC, MODE>;
-  const int smem = S::smem(a.c.keep_ch0 != 0);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kern<<<kSms, S::WARPS * 32, smem, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_ch0(const PagedDecodeArgs& a, cudaStream_t s) {
+  return a.c.keep_ch0 ? launch_one<KB, VB, HC, MODE, true>(a, s) : launch_one<KB, VB, HC, MODE, false>(a, s);
 }
 
 template <int KB, int VB, int HC>
 cudaError_t launch_type(const PagedDecodeArgs& a, cudaStream_t s) {
-  if (a.dtype == KVQ_F32) return launch_one<KB, VB, HC, kF32>(a, s);
-  return a.dtype == KVQ_F16 ? launch_one<KB, VB, HC, kF16>(a, s) : launch_one<KB, VB, HC, kBf16>(a, s);
+  if (a.dtype == KVQ_F32) return launch_ch0<KB, VB, HC, kF32>(a, s);
+  return a.dtype == KVQ_F16 ? launch_ch0<KB, VB, HC, kF16>(a, s) : launch_ch0<KB, VB, HC, kBf16>(a, s);
 }
 
 template <int KB, int VB>

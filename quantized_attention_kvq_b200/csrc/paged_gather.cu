@@ -1,9 +1,11 @@
 // Dense rows of cached tokens: the mirror of the paged append.
 //
-// A warp takes 8 tokens of one head's keys (or values), four lanes per token,
-// lane g owning 32 channels; a lane reads its codes' bytes, forms
-// scale * code + zero with one rounding, takes the row back through the
-// transform in fp32 when asked and writes its 32 channels in 16-byte pieces.
+// A warp takes 8 tokens of one head's keys (or values), four lanes per token;
+// lane g holds channels 32k + 8g .. 32k + 8g + 7 of every quantization group k,
+// so that each store of a warp covers whole 64-byte pieces of its rows (one
+// group per lane measured 43 us instead of the figure below: half-written
+// sectors).  A lane reads its codes' bytes, forms scale * code + zero with one
+// rounding and takes the row back through the transform in fp32 when asked.
 #include "paged.cuh"
 
 namespace kvq {
@@ -11,7 +13,9 @@ namespace {
 
 constexpr int kGatherWarps = 4;
 
-// Orthonormal Walsh-Hadamard transform of a row held by four lanes, in fp32
+// Orthonormal Walsh-Hadamard transform of a row held by four lanes as above, in
+// fp32: x[8k + r] is channel 32k + 8g + r, so the stages 1, 2, 4, 32 and 64 stay in
+// the lane and 8 and 16 pair lanes g ^ 1 and g ^ 2
 __device__ __forceinline__ void rotate_row_4lanes_f32(float (&x)[32], int g) {
 #pragma unroll
   for (int hs = 1; hs < 32; hs <<= 1)
@@ -30,6 +34,15 @@ __device__ __forceinline__ void rotate_row_4lanes_f32(float (&x)[32], int g) {
   }
 #pragma unroll
   for (int i = 0; i < 32; ++i) x[i] *= 0.08838834764831845f;  // 1 / sqrt(128)
+}
+
+// four fp16 of one token as floats
+__device__ __forceinline__ void halves4(uint2 v, float (&f)[4]) {
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+  f[0] = a.x;
+  f[1] = a.y;
+  f[2] = b.x;
+  f[3] = b.y;
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16*) {
@@ -61,43 +74,58 @@ __global__ void __launch_bounds__(kGatherWarps * 32) k_paged_gather(PagedGatherA
 #pragma unroll
   for (int i = 0; i < 32; ++i) x[i] = 0.0f;
   if (read && !values) {
-    const float s = __half2float(reinterpret_cast<const __half*>(blk + lay.ks)[scale_index(t, g)]);
-    const float z = __half2float(reinterpret_cast<const __half*>(blk + lay.kz)[k_zero_index(t, g)]);
+    float sc[4], zr[4];
+    halves4(*reinterpret_cast<const uint2*>(blk + lay.ks + 2 * scale_index(t, 0)), sc);
+    halves4(make_uint2(*reinterpret_cast<const uint32_t*>(blk + lay.kz + 2 * k_zero_index(t, 0)),
+                       *reinterpret_cast<const uint32_t*>(blk + lay.kz + 2 * k_zero_index(t, 2))), zr);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const uint8_t* d = blk + k_code_byte(KB, 8 * g + r, t);
-      const uint32_t w = KB == 4 ? (uint32_t)d[0] | ((uint32_t)d[2] << 8) : (uint32_t)d[0];
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[4 * r + j] = fmaf(s, (float)((w >> (KB * j)) & ((1 << KB) - 1)), z);
-    }
+      for (int r = 0; r < 2; ++r) {
+        const uint8_t* d = blk + k_code_byte(KB, 8 * k + 2 * g + r, t);
+        uint32_t w;
+        if (KB == 4) {  // the token's two bytes sit in one word
+          w = *reinterpret_cast<const uint32_t*>(d - (t & 1)) >> (8 * (t & 1));
+          w = __byte_perm(w, 0, 0x4420);
+        } else {
+          w = d[0];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[8 * k + 4 * r + j] = fmaf(sc[k], (float)((w >> (KB * j)) & ((1 << KB) - 1)), zr[k]);
+      }
     if (c.keep_ch0 && g == 0) x[0] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(blk + lay.k0)[t]);
   } else if (read) {
-    const float s = __half2float(reinterpret_cast<const __half*>(blk + lay.vs)[scale_index(t, g)]);
-    const float z = __half2float(reinterpret_cast<const __half*>(blk + lay.vz)[scale_index(t, g)]);
+    float sc[4], zr[4];
+    halves4(*reinterpret_cast<const uint2*>(blk + lay.vs + 2 * scale_index(t, 0)), sc);
+    halves4(*reinterpret_cast<const uint2*>(blk + lay.vz + 2 * scale_index(t, 0)), zr);
     const uint8_t* d = blk + lay.vc + v_token_byte(t);
+    constexpr int PER = 8 / VB;  // channels per byte
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const uint32_t w = VB == 4 ? (uint32_t)d[(16 * g + 2 * r) * 64] | ((uint32_t)d[(16 * g + 2 * r + 1) * 64] << 8)
-                                 : (uint32_t)d[(8 * g + r) * 64];
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[4 * r + j] = fmaf(s, (float)((w >> (VB * j)) & ((1 << VB) - 1)), z);
-    }
+      for (int r = 0; r < 8 / PER; ++r) {
+        const uint32_t w = d[((32 * k + 8 * g) / PER + r) * 64];
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          x[8 * k + PER * r + j] = fmaf(sc[k], (float)((w >> (VB * j)) & ((1 << VB) - 1)), zr[k]);
+      }
   }
   if (a.rotate_back && (values ? c.rotate_v : c.rotate_k)) rotate_row_4lanes_f32(x, g);
   if (tok >= a.n) return;
-  Out* dst = static_cast<Out*>(values ? a.v : a.k) + ((size_t)tok * c.H + h) * kHeadDim + 32 * g;
-  uint4* d = reinterpret_cast<uint4*>(dst);
-  if constexpr (sizeof(Out) == 4) {
+  Out* dst = static_cast<Out*>(values ? a.v : a.k) + ((size_t)tok * c.H + h) * kHeadDim + 8 * g;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      d[i] = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]),
-                        __float_as_uint(x[4 * i + 3]));
-  } else {
-    Out* ty = nullptr;
+  for (int k = 0; k < 4; ++k) {
+    uint4* d = reinterpret_cast<uint4*>(dst + 32 * k);
+    if constexpr (sizeof(Out) == 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      d[i] = make_uint4(pack2(x[8 * i], x[8 * i + 1], ty), pack2(x[8 * i + 2], x[8 * i + 3], ty),
-                        pack2(x[8 * i + 4], x[8 * i + 5], ty), pack2(x[8 * i + 6], x[8 * i + 7], ty));
+      for (int i = 0; i < 2; ++i)
+        d[i] = make_uint4(__float_as_uint(x[8 * k + 4 * i]), __float_as_uint(x[8 * k + 4 * i + 1]),
+                          __float_as_uint(x[8 * k + 4 * i + 2]), __float_as_uint(x[8 * k + 4 * i + 3]));
+    } else {
+      Out* ty = nullptr;
+      d[0] = make_uint4(pack2(x[8 * k], x[8 * k + 1], ty), pack2(x[8 * k + 2], x[8 * k + 3], ty),
+                        pack2(x[8 * k + 4], x[8 * k + 5], ty), pack2(x[8 * k + 6], x[8 * k + 7], ty));
+    }
   }
 }
 

@@ -358,18 +358,13 @@ class KVQCache:
 
 
 def _device_of(*tensors: torch.Tensor | None) -> int:
-    """Index of the one CUDA device all the tensors are on."""
-    dev = None
+    """Index of the one CUDA device all the tensors are on (the first is not None)."""
+    dev = tensors[0].get_device()  # -1 for a host tensor
     for t in tensors:
-        if t is None:
-            continue
-        d = t.get_device()  # -1 for a host tensor
-        if d < 0:
-            raise ValueError("expected a CUDA tensor (the library has no CPU path)")
-        if dev is None:
-            dev = d
-        elif d != dev:
-            raise ValueError(f"tensors on cuda:{dev} and cuda:{d}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {tensors[0].device} and {t.device}")
+    if dev < 0:
+        raise ValueError("expected CUDA tensors (the library has no CPU path)")
     return dev
 
 
@@ -427,21 +422,30 @@ class PagePlanner:
         [num_pages], both updated in place; free_count: int32 [1].  Returns the new tokens' slots and
         positions [n_slots], cu_new [B + 1], the sequence lengths [B] and the free pages left [1]; `out`
         reuses an earlier plan's tensors (its seq_lens may be ctx_lens, its free_count free_count)."""
-        if ctx_lens.dim() != 1 or block_table.dim() != 2:
-            raise ValueError("ctx_lens is [B], block_table [B][max_pages]")
+        if block_table.dim() != 2:
+            raise ValueError("block_table is [B][max_pages]")
         B, max_pages = block_table.shape
-        ctx = _i32(ctx_lens, "ctx_lens", B)
-        if out is None:
-            out = PagePlan(ctx_lens.new_empty(n_slots), ctx_lens.new_empty(n_slots), ctx_lens.new_empty(B + 1),
-                           ctx_lens.new_empty(B), ctx_lens.new_empty(1))
-        dev = _device_of(ctx_lens, new_lens, block_table, free_pages, free_count, done, out.slots, out.positions,
-                         out.cu_new, out.seq_lens, out.free_count)
-        _call(dev, stream, "kvq_page_plan", lib().kvq_page_plan, self.num_pages, self.page_tokens, B, ctx,
-              _i32(new_lens, "new_lens", B), _i32(done, "done", B), _i32(block_table, "block_table", B, max_pages),
-              max_pages, _i32(free_pages, "free_pages", self.num_pages), _i32(free_count, "free_count", 1),
-              _i32(out.free_count, "free_count", 1), _i32(out.slots, "slots", n_slots),
-              _i32(out.positions, "positions", n_slots), n_slots, _i32(out.cu_new, "cu_new", B + 1),
-              _i32(out.seq_lens, "seq_lens", B))
+        dev = _device_of(ctx_lens, new_lens, block_table, free_pages, free_count, done)
+        if out is None:  # one allocation, its tensors one after another
+            head = (2 * B + 5) & ~3  # cu_new, seq_lens and free_count, then 16-byte aligned slots and positions
+            tail = (n_slots + 3) & ~3
+            buf = ctx_lens.new_empty(head + 2 * tail)
+            c, s, f, _, n, _, p, _ = buf.split_with_sizes((B + 1, B, 1, head - 2 * B - 2, n_slots, tail - n_slots, n_slots,
+                                                           tail - n_slots))
+            out = PagePlan(n, p, c, s, f)
+            cu = buf.data_ptr()
+            lens, left, slots = cu + 4 * (B + 1), cu + 4 * (2 * B + 1), cu + 4 * head
+            pos = slots + 4 * tail
+        else:
+            _device_of(ctx_lens, out.slots, out.positions, out.cu_new, out.seq_lens, out.free_count)
+            slots, pos = _i32(out.slots, "slots", n_slots), _i32(out.positions, "positions", n_slots)
+            cu, lens = _i32(out.cu_new, "cu_new", B + 1), _i32(out.seq_lens, "seq_lens", B)
+            left = _i32(out.free_count, "free_count", 1)
+        _call(dev, stream, "kvq_page_plan", lib().kvq_page_plan, self.num_pages, self.page_tokens, B,
+              _i32(ctx_lens, "ctx_lens", B), _i32(new_lens, "new_lens", B), _i32(done, "done", B),
+              _i32(block_table, "block_table", B, max_pages), max_pages,
+              _i32(free_pages, "free_pages", self.num_pages), _i32(free_count, "free_count", 1), left, slots, pos, n_slots,
+              cu, lens)
         return out
 
 
@@ -482,15 +486,17 @@ class PagedKVQCache:
     def gather(self, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16, rotate_back: bool = True,
                k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, stream=None):
         """The cached tokens' keys and values as dense rows [n][H][128] of `dtype`."""
-        n, shape = slots.shape[0], (slots.shape[0], self.H, 128)
-        if k_out is None:
-            k_out = torch.empty(shape, dtype=dtype, device=slots.device)
-        if v_out is None:
-            v_out = torch.empty(shape, dtype=dtype, device=slots.device)
-        for t in (k_out, v_out):
-            if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
-                raise ValueError(f"k_out and v_out are contiguous {list(shape)} of {dtype}")
+        n = slots.shape[0]
+        shape = (n, self.H, 128)
         dev = _device_of(slots, k_out, v_out, self.pages)
+        if k_out is None:
+            k_out = slots.new_empty(shape, dtype=dtype)
+        elif k_out.shape != shape or k_out.dtype is not dtype or not k_out.is_contiguous():
+            raise ValueError(f"k_out is a contiguous {list(shape)} of {dtype}")
+        if v_out is None:
+            v_out = slots.new_empty(shape, dtype=dtype)
+        elif v_out.shape != shape or v_out.dtype is not dtype or not v_out.is_contiguous():
+            raise ValueError(f"v_out is a contiguous {list(shape)} of {dtype}")
         _call(dev, stream, "kvq_paged_gather", lib().kvq_paged_gather, self._ref, _i32(slots, "slots", n), n,
               torch_dtype_code(dtype), int(rotate_back), k_out.data_ptr(), v_out.data_ptr())
         return k_out, v_out
@@ -519,20 +525,20 @@ class PagedKVQCache:
         returns [B][Hq][128] of q's type."""
         if q.dim() != 3 or block_table.dim() != 2:
             raise ValueError("q is [B][Hq][128], block_table [B][max_pages]")
-        B, Hq = q.shape[0], q.shape[1]
+        B, Hq, _ = q.shape
         qp, qs = _rows(q, "q", Hq)
+        dev = _device_of(q, block_table, seq_lens, mask, out, workspace, self.pages)
         if out is None:
-            out = torch.empty((B, Hq, 128), dtype=q.dtype, device=q.device)
+            out = q.new_empty((B, Hq, 128))
         elif out.shape != (B, Hq, 128) or out.dtype is not q.dtype or not out.is_contiguous():
             raise ValueError(f"out is a contiguous [{B}][{Hq}][128] of {q.dtype}")
         if workspace is None:
-            workspace = torch.empty(max(self.workspace_bytes(B, Hq), 256), dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty(max(self.workspace_bytes(B, Hq), 256), dtype=torch.uint8)
         elif not workspace.is_contiguous():
             raise ValueError("workspace is contiguous")
-        dev = _device_of(q, block_table, seq_lens, mask, out, workspace, self.pages)
         max_pages = block_table.shape[1]
-        _call(dev, stream, "kvq_paged_decode", lib().kvq_paged_decode, self._ref, qp, qs, torch_dtype_code(q.dtype), Hq,
-              B, _i32(block_table, "block_table", B, max_pages), max_pages, _i32(seq_lens, "seq_lens", B), max_len,
+        _call(dev, stream, "kvq_paged_decode", lib().kvq_paged_decode, self._ref, qp, qs, _DTYPE_CODES[q.dtype], Hq, B,
+              _i32(block_table, "block_table", B, max_pages), max_pages, _i32(seq_lens, "seq_lens", B), max_len,
               _i32(mask, "mask", B, self.H), 0.08838834764831845 if softmax_scale is None else softmax_scale,
               out.data_ptr(), workspace.data_ptr(), workspace.nbytes)
         return out
