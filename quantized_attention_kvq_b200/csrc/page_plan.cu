@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PlanArgs a) {
   int* need = cu + B + 1;       // [B + 1] pages needed before request b
   int* give = need + B + 1;     // [B + 1] pages given back before request b
   int* ctx = give + B + 1;      // [B] cached tokens, 0 for finished requests
-  __shared__ long long wsum[3][kPlanThreads / 32];
+  __shared__ long long wsum[2][kPlanThreads / 32];
   __shared__ int taken_s;
   const int count = min(max(*a.count, 0), a.num_pages);
 
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PlanArgs a) {
   const int per = (B + kPlanThreads - 1) / kPlanThreads;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
   constexpr long long kMax = 0x7FFFFFFF;
-  long long s[3] = {0, 0, 0};
+  long long s[2] = {0, 0};
   const long long row_tokens = (long long)a.max_pages * P;
   // pass 0: new tokens and pages given back; pass 1: pages needed, which depend on cu
   for (int pass = 0; pass < 2; ++pass) {
@@ -90,12 +90,22 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PlanArgs a) {
       wsum[1][tid >> 5] = x1;
     }
     __syncthreads();
-    s[0] = x0 - t0;
-    s[1] = x1 - t1;
-    for (int w = 0; w < (tid >> 5); ++w) {
-      s[0] += wsum[0][w];
-      s[1] += wsum[1][w];
+    // every warp scans the warps' totals for itself
+    long long y0 = wsum[0][tid & 31], y1 = wsum[1][tid & 31];
+    static_assert(kPlanThreads == 1024, "one total per lane");
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long z0 = __shfl_up_sync(kFull, y0, m), z1 = __shfl_up_sync(kFull, y1, m);
+      if ((tid & 31) >= m) {
+        y0 += z0;
+        y1 += z1;
+      }
     }
+    const int prev = (tid >> 5) - 1;
+    y0 = __shfl_sync(kFull, y0, prev & 31);
+    y1 = __shfl_sync(kFull, y1, prev & 31);
+    s[0] = x0 - t0 + (prev >= 0 ? y0 : 0);
+    s[1] = x1 - t1 + (prev >= 0 ? y1 : 0);
     int* out0 = pass == 0 ? cu : need;
     if (tid == 0) {
       out0[0] = 0;

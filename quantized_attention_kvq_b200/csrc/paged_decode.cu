@@ -24,20 +24,19 @@ __global__ void __launch_bounds__(256) k_paged_combine(PagedDecodeArgs a, int ma
   __shared__ float2 sml[8];
   __shared__ float4 sacc[8][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * (8 / WPR) + warp / WPR;
+  const int row = (int)blockIdx.x * (8 / WPR) + warp / WPR;
   const int part = warp % WPR;
-  const bool live = row < (long long)a.B * a.Hq;
+  const bool live = row < a.B * a.Hq;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the split decode's partials are complete
   float m = -INFINITY, l = 0.0f;
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (live) {
-    const int b = (int)(row / a.Hq), j = (int)(row % a.Hq), H = a.c.H, h = j / a.G, hd = j - h * a.G;
-    const long long total = (long long)a.starts[a.B] * H;
+    const int b = row / a.Hq, j = row - b * a.Hq, H = a.c.H, h = j / a.G, hd = j - h * a.G;
+    const int total = a.starts[a.B] * H;
     const int s0 = a.starts[b], tiles = a.starts[b + 1] - s0;
     if (tiles > 0) {
-      const long long ranks = min((long long)max_ranks, total);
-      const long long x = (long long)s0 * H + (long long)h * tiles;
-      const int r0 = (int)(((x + 1) * ranks - 1) / total), r1 = (int)(((x + tiles) * ranks - 1) / total);
+      const int ranks = min(max_ranks, total), x = s0 * H + h * tiles;
+      const int r0 = rank_of(x, ranks, total), r1 = rank_of(x + tiles - 1, ranks, total);
       const size_t unit = (size_t)b * H + h;
       constexpr int U = 8;  // partials in flight per warp
       for (int r = r0 + part; r <= r1; r += U * WPR) {

@@ -201,6 +201,16 @@ __device__ __forceinline__ int tiles_of(const PagedDecodeArgs& a, int b) {
   return (len + kBlockTokens - 1) / kBlockTokens;
 }
 
+// Ranks cut `total` tiles evenly: rank r takes tiles [r total / ranks, (r + 1) total /
+// ranks).  In fp64: the products are below 2^53 and a quotient that is no whole
+// number is at least 2^-31 from one, so rounding it down is exact.
+__device__ __forceinline__ int first_tile(int rank, int ranks, int total) {
+  return (int)((double)rank * total / ranks);
+}
+__device__ __forceinline__ int rank_of(int tile, int ranks, int total) {
+  return (int)((((double)tile + 1.0) * ranks - 1.0) / total);
+}
+
 // One tile of a warp's range, as its lanes leave it in shared memory (16 bytes)
 struct Tile {
   int block;     // its block's number in the pool, -1: the page is outside the pool
@@ -279,7 +289,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
     if (lane == 0) a.status[rank] = 0;
     return;
   }
-  const int t0 = (int)((long long)rank * total / ranks), n = (int)((long long)(rank + 1) * total / ranks) - t0;
+  const int t0 = first_tile(rank, ranks, total), n = first_tile(rank + 1, ranks, total) - t0;
 
   // ---- one lane looks up one tile, 32 tiles at a time
   auto look_up = [&](int k) {

@@ -36,6 +36,14 @@ __device__ __forceinline__ void rotate_row_4lanes_f32(float (&x)[32], int g) {
   for (int i = 0; i < 32; ++i) x[i] *= 0.08838834764831845f;  // 1 / sqrt(128)
 }
 
+// The code at bits [sh, sh + BITS) of a word of at most 16 bits, times 2^sh, as a
+// float: under the significand of 2^23 it needs no conversion, only a subtraction
+// (and the scale takes 2^-sh)
+template <int BITS>
+__device__ __forceinline__ float field_of(uint32_t w, int sh) {
+  return __uint_as_float((w & (((1u << BITS) - 1u) << sh)) | 0x4B000000u) - 8388608.0f;
+}
+
 // four fp16 of one token as floats
 __device__ __forceinline__ void halves4(uint2 v, float (&f)[4]) {
   const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
@@ -91,7 +99,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32) k_paged_gather(PagedGatherA
           w = d[0];
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[8 * k + 4 * r + j] = fmaf(sc[k], (float)((w >> (KB * j)) & ((1 << KB) - 1)), zr[k]);
+        for (int j = 0; j < 4; ++j) x[8 * k + 4 * r + j] = fmaf(sc[k] * (1.0f / (1 << (KB * j))), field_of<KB>(w, KB * j), zr[k]);
       }
     if (c.keep_ch0 && g == 0) x[0] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(blk + lay.k0)[t]);
   } else if (read) {
@@ -107,7 +115,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32) k_paged_gather(PagedGatherA
         const uint32_t w = d[((32 * k + 8 * g) / PER + r) * 64];
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-          x[8 * k + PER * r + j] = fmaf(sc[k], (float)((w >> (VB * j)) & ((1 << VB) - 1)), zr[k]);
+          x[8 * k + PER * r + j] = fmaf(sc[k] * (1.0f / (1 << (VB * j))), field_of<VB>(w, VB * j), zr[k]);
       }
   }
   if (a.rotate_back && (values ? c.rotate_v : c.rotate_k)) rotate_row_4lanes_f32(x, g);

@@ -471,6 +471,8 @@ class PagedKVQCache:
         self.desc.pages = _dev_ptr(pages)
         self.num_pages, self.H, self.page_tokens = num_pages, H, page_tokens
         self.planner = PagePlanner(num_pages, page_tokens)
+        L = lib()
+        self._decode, self._append, self._gather = L.kvq_paged_decode, L.kvq_paged_append, L.kvq_paged_gather
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor, stream=None):
         """k_new, v_new: [n][H][128] (fp32 / bf16 / fp16), rows at any 16-byte stride; slots: int32 [n]."""
@@ -480,7 +482,7 @@ class PagedKVQCache:
         k, ks = _rows(k_new, "k_new", self.H)
         v, vs = _rows(v_new, "v_new", self.H)
         n = k_new.shape[0]
-        _call(dev, stream, "kvq_paged_append", lib().kvq_paged_append, self._ref, k, ks, v, vs,
+        _call(dev, stream, "kvq_paged_append", self._append, self._ref, k, ks, v, vs,
               torch_dtype_code(k_new.dtype), n, _i32(slots, "slots", n))
 
     def gather(self, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16, rotate_back: bool = True,
@@ -497,7 +499,7 @@ class PagedKVQCache:
             v_out = slots.new_empty(shape, dtype=dtype)
         elif v_out.shape != shape or v_out.dtype is not dtype or not v_out.is_contiguous():
             raise ValueError(f"v_out is a contiguous {list(shape)} of {dtype}")
-        _call(dev, stream, "kvq_paged_gather", lib().kvq_paged_gather, self._ref, _i32(slots, "slots", n), n,
+        _call(dev, stream, "kvq_paged_gather", self._gather, self._ref, _i32(slots, "slots", n), n,
               torch_dtype_code(dtype), int(rotate_back), k_out.data_ptr(), v_out.data_ptr())
         return k_out, v_out
 
@@ -523,8 +525,6 @@ class PagedKVQCache:
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """q: [B][Hq][128], rows at any 16-byte stride; block_table: int32 [B][max_pages]; seq_lens: int32 [B];
         returns [B][Hq][128] of q's type."""
-        if q.dim() != 3 or block_table.dim() != 2:
-            raise ValueError("q is [B][Hq][128], block_table [B][max_pages]")
         B, Hq, _ = q.shape
         qp, qs = _rows(q, "q", Hq)
         dev = _device_of(q, block_table, seq_lens, mask, out, workspace, self.pages)
@@ -536,11 +536,12 @@ class PagedKVQCache:
             workspace = q.new_empty(max(self.workspace_bytes(B, Hq), 256), dtype=torch.uint8)
         elif not workspace.is_contiguous():
             raise ValueError("workspace is contiguous")
-        max_pages = block_table.shape[1]
-        _call(dev, stream, "kvq_paged_decode", lib().kvq_paged_decode, self._ref, qp, qs, _DTYPE_CODES[q.dtype], Hq, B,
+        max_pages = block_table.shape[-1]
+        _call(dev, stream, "kvq_paged_decode", self._decode, self._ref, qp, qs, _DTYPE_CODES[q.dtype], Hq, B,
               _i32(block_table, "block_table", B, max_pages), max_pages, _i32(seq_lens, "seq_lens", B), max_len,
-              _i32(mask, "mask", B, self.H), 0.08838834764831845 if softmax_scale is None else softmax_scale,
-              out.data_ptr(), workspace.data_ptr(), workspace.nbytes)
+              None if mask is None else _i32(mask, "mask", B, self.H),
+              0.08838834764831845 if softmax_scale is None else softmax_scale, out.data_ptr(), workspace.data_ptr(),
+              workspace.nbytes)
         return out
 
     def decode_status(self, batch: int, q_heads: int, workspace: torch.Tensor, stream=None) -> int:
