@@ -51,6 +51,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PlanArgs a) {
   int* ctx = give + B + 1;      // [B] cached tokens, 0 for finished requests
   __shared__ long long wsum[2][kPlanThreads / 32];
   __shared__ int taken_s;
+  let_next_start();
+  wait_for_stream();
   const int count = min(max(*a.count, 0), a.num_pages);
 
   // each thread sums a run of consecutive requests; the runs are joined by a
@@ -224,12 +226,14 @@ cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t s) {
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = ctas;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k_page_plan, a);
 }
 

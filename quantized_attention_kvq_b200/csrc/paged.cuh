@@ -60,6 +60,28 @@ struct PagedView {
   }
 };
 
+// The paged kernels are launched so that each may take its place on the SMs while
+// the kernel before it in the stream drains (programmatic stream serialization):
+// wait_for_stream() before the first access to global memory waits until that
+// kernel has completed, let_next_start() allows the next one to be placed.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... Args>
+cudaError_t launch_overlapped(void (*kern)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 struct PlanArgs {
   int num_pages, page_tokens, batch, max_pages, n_slots;
   const int32_t *ctx, *add, *done;

@@ -100,6 +100,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendBlocks) k_paged_appe
   const int tok = (blockIdx.x * kAppendWarps + warp) * 8 + (lane >> 2);
   const int h = blockIdx.y;
   const bool values = blockIdx.z != 0;
+  let_next_start();
+  wait_for_stream();
   const int slot = tok < a.n ? a.slots[tok] : -1;
   const bool active = slot >= 0 && slot < c.slots();
   // the row is loaded beside its slot; lanes behind the last token work on the
@@ -158,13 +160,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendBlocks) k_paged_appe
 template <int KB, int VB>
 cudaError_t launch_typed(const PagedAppendArgs& a, cudaStream_t s) {
   const dim3 grid((a.n + 8 * kAppendWarps - 1) / (8 * kAppendWarps), a.c.H, 2), block(32 * kAppendWarps);
-  if (a.dtype == KVQ_F32)
-    k_paged_append<KB, VB, float><<<grid, block, 0, s>>>(a);
-  else if (a.dtype == KVQ_BF16)
-    k_paged_append<KB, VB, __nv_bfloat16><<<grid, block, 0, s>>>(a);
-  else
-    k_paged_append<KB, VB, __half><<<grid, block, 0, s>>>(a);
-  return cudaGetLastError();
+  if (a.dtype == KVQ_F32) return launch_overlapped(k_paged_append<KB, VB, float>, grid, block, 0, s, a);
+  if (a.dtype == KVQ_BF16) return launch_overlapped(k_paged_append<KB, VB, __nv_bfloat16>, grid, block, 0, s, a);
+  return launch_overlapped(k_paged_append<KB, VB, __half>, grid, block, 0, s, a);
 }
 
 }  // namespace

@@ -27,7 +27,8 @@ __global__ void __launch_bounds__(256) k_paged_combine(PagedDecodeArgs a, int ma
   const int row = (int)blockIdx.x * (8 / WPR) + warp / WPR;
   const int part = warp % WPR;
   const bool live = row < a.B * a.Hq;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the split decode's partials are complete
+  let_next_start();
+  wait_for_stream();  // the split decode's partials are complete
   float m = -INFINITY, l = 0.0f;
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (live) {
@@ -38,7 +39,7 @@ __global__ void __launch_bounds__(256) k_paged_combine(PagedDecodeArgs a, int ma
       const int ranks = min(max_ranks, total), x = s0 * H + h * tiles;
       const int r0 = rank_of(x, ranks, total), r1 = rank_of(x + tiles - 1, ranks, total);
       const size_t unit = (size_t)b * H + h;
-      constexpr int U = 8;  // partials in flight per warp
+      constexpr int U = WPR == 1 ? 2 : 8;  // partials in flight per warp
       for (int r = r0 + part; r <= r1; r += U * WPR) {
         float2 ml[U];
         float4 v[U];
@@ -132,16 +133,8 @@ cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t s) {
   // sequence was cut into many
   const long long units = (long long)a.B * a.c.H, rows = (long long)a.B * a.Hq;
   const bool many = ranks / units >= 8;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(many ? rows : (rows + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return many ? cudaLaunchKernelEx(&cfg, k_paged_combine<8>, a, ranks) : cudaLaunchKernelEx(&cfg, k_paged_combine<1>, a, ranks);
+  if (many) return launch_overlapped(k_paged_combine<8>, dim3((unsigned)rows), dim3(256), 0, s, a, ranks);
+  return launch_overlapped(k_paged_combine<1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a, ranks);
 }
 
 unsigned bounds_paged_decode(bool reset) {

@@ -81,7 +81,8 @@ struct Shape {
   static constexpr int TILES = 64 * 16;           // what is known of the warp's next tiles
   static constexpr int ROWS = 32;                 // the kept key rows, one byte each
   static constexpr int WARP_FIXED = QF + QZ + QH + TILES + ROWS;
-  static constexpr int F_WTOT = (THREADS + 4) * 4;
+  static constexpr int F_LENS = (THREADS + 4) * 4;  // after the tiles before each chunk of requests: their lengths
+  static constexpr int F_WTOT = F_LENS + THREADS * 4;
   static constexpr int F_BARS = F_WTOT + 64;
   static constexpr int F_WARP = F_BARS + WARPS * 2 * kMaxSlots * 8;
   static constexpr int RING = (F_WARP + WARPS * WARP_FIXED + 127) / 128 * 128;
@@ -201,14 +202,14 @@ __device__ __forceinline__ int tiles_of(const PagedDecodeArgs& a, int b) {
   return (len + kBlockTokens - 1) / kBlockTokens;
 }
 
-// Ranks cut `total` tiles evenly: rank r takes tiles [r total / ranks, (r + 1) total /
-// ranks).  In fp64: the products are below 2^53 and a quotient that is no whole
-// number is at least 2^-31 from one, so rounding it down is exact.
+// Ranks cut `total` tiles evenly, the first total % ranks taking one tile more
 __device__ __forceinline__ int first_tile(int rank, int ranks, int total) {
-  return (int)((double)rank * total / ranks);
+  const int base = total / ranks;
+  return rank * base + min(rank, total - base * ranks);
 }
 __device__ __forceinline__ int rank_of(int tile, int ranks, int total) {
-  return (int)((((double)tile + 1.0) * ranks - 1.0) / total);
+  const int base = total / ranks, more = total - base * ranks, cut = more * (base + 1);
+  return tile < cut ? tile / (base + 1) : more + (tile - cut) / base;
 }
 
 // One tile of a warp's range, as its lanes leave it in shared memory (16 bytes)
@@ -232,36 +233,23 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
   const int g = lane >> 2, cq = lane & 3;
   constexpr int SK = S::SK, SV = S::SV;
 
-  // ---- tiles per request: chunk prefix sums over the batch
-  int* chunk = reinterpret_cast<int*>(smem);  // [TH + 1] tiles before each chunk of requests
+  // ---- the requests' tiles: prefix sums over chunks of requests (a chunk is one
+  // request up to a batch of TH, whose lengths then stay in shared memory).  The
+  // start of the kernel is one chain of memory latencies (lengths, block table,
+  // pages), so what does not need the lengths is done while they are on their way.
+  int* chunk = reinterpret_cast<int*>(smem);  // [TH + 1] tiles before each chunk
+  int* lens_s = reinterpret_cast<int*>(smem + S::F_LENS);
   int* wtot = reinterpret_cast<int*>(smem + S::F_WTOT);
   const int per_chunk = (a.B + TH - 1) / TH;
+  const int cb0 = min(tid * per_chunk, a.B), cb1 = min(cb0 + per_chunk, a.B);
+  wait_for_stream();
+  const int len0 = cb0 < cb1 ? a.lens[cb0] : 0;
+  // the block table on its way to L2: each CTA asks for some of its lines
   {
-    int mine = 0;
-    const int b0 = min(tid * per_chunk, a.B), b1 = min(b0 + per_chunk, a.B);
-    for (int b = b0; b < b1; ++b) mine += tiles_of(a, b);
-    int x = mine;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const int y = __shfl_up_sync(kFull, x, m);
-      if (lane >= m) x += y;
-    }
-    if (lane == 31) wtot[warp] = x;
-    __syncthreads();
-    int before = x - mine;
-    for (int w = 0; w < warp; ++w) before += wtot[w];
-    chunk[tid] = before;
-    if (tid == TH - 1) chunk[TH] = before + mine;
-    if (blockIdx.x == 0) {  // for the combine
-      for (int b = b0; b < b1; ++b) {
-        a.starts[b] = before;
-        before += tiles_of(a, b);
-      }
-      if (tid == TH - 1) a.starts[a.B] = chunk[TH];
-    }
-    if (warp == 0 && lane == 0)  // status words of ranks other shapes have
-      for (int r = W * kSms + blockIdx.x; r < kPagedMaxRanks; r += kSms) a.status[r] = 0;
+    const long long line = blockIdx.x + (long long)kSms * tid, at = line * 32;  // 32 entries
+    if (at < (long long)a.B * a.max_pages) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.table + at));
   }
+
   const uint32_t kbars = smem_addr(smem + S::F_BARS) + warp * 2 * kMaxSlots * 8, vbars = kbars + kMaxSlots * 8;
   uint8_t* mine = smem + S::F_WARP + warp * S::WARP_FIXED;
   uint32_t* qf = reinterpret_cast<uint32_t*>(mine);                  // [8][NT][32] x {b0, b1}
@@ -271,7 +259,10 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
   uint8_t* kept = reinterpret_cast<uint8_t*>(tiles + 64);               // [32] kept key rows of the issue's unit
   uint8_t* kring = smem + S::RING + warp * S::WARP_RING;
   uint8_t* vring = kring + SK * S::KPART;
-  for (int i = lane; i < (S::QF + S::QZ + S::QH) / 4; i += 32) qf[i] = 0;  // columns of absent heads stay zero
+  static_assert(S::WARP_FIXED % 16 == 0 && (S::QF + S::QZ + S::QH) % 16 == 0 && S::F_WARP % 16 == 0, "16-byte stores");
+#pragma unroll 4
+  for (int i = lane; i < (S::QF + S::QZ + S::QH) / 16; i += 32)  // columns of absent heads stay zero
+    reinterpret_cast<uint4*>(mine)[i] = make_uint4(0, 0, 0, 0);
   if (lane == 0) {
     // with a mask every lane copies key rows and arrives beside the bulk copy of the rest
     for (int s = 0; s < kMaxSlots; ++s) {
@@ -279,6 +270,39 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
       mbar_init(vbars + 8 * s, 1);
     }
     mbar_fence_init();
+  }
+  {
+    const int len = min(max(len0, 0), a.max_len);
+    lens_s[tid] = len;
+    int own = (len + kBlockTokens - 1) / kBlockTokens;
+    for (int b = cb0 + 1; b < cb1; ++b) own += tiles_of(a, b);
+    int x = own;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int y = __shfl_up_sync(kFull, x, m);
+      if (lane >= m) x += y;
+    }
+    if (lane == 31) wtot[warp] = x;
+    __syncthreads();
+    int t = lane < W ? wtot[lane] : 0;  // every warp scans the warps' totals for itself
+#pragma unroll
+    for (int m = 1; m < W; m <<= 1) {
+      const int y = __shfl_up_sync(kFull, t, m);
+      if (lane >= m) t += y;
+    }
+    const int prev = __shfl_sync(kFull, t, (warp + 31) & 31);
+    int before = x - own + (warp > 0 ? prev : 0);
+    chunk[tid] = before;
+    if (tid == TH - 1) chunk[TH] = before + own;
+    if (blockIdx.x == 0) {  // for the combine
+      for (int b = cb0; b < cb1; ++b) {
+        a.starts[b] = before;
+        before += tiles_of(a, b);
+      }
+      if (tid == TH - 1) a.starts[a.B] = chunk[TH];
+    }
+    if (warp == 0 && lane == 0)  // status words of ranks other shapes have
+      for (int r = W * kSms + blockIdx.x; r < kPagedMaxRanks; r += kSms) a.status[r] = 0;
   }
   __syncthreads();
 
@@ -304,15 +328,22 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
         else
           hi = m;
       }
-      int b = lo * per_chunk, r = ti - chunk[lo] * c.H, tb = tiles_of(a, b);
-      while (r >= tb * c.H) {
-        r -= tb * c.H;
-        tb = tiles_of(a, ++b);
+      int b = lo * per_chunk, r = ti - chunk[lo] * c.H, tb, len;
+      if (per_chunk == 1) {
+        tb = chunk[lo + 1] - chunk[lo];
+        len = lens_s[lo];
+      } else {
+        tb = tiles_of(a, b);
+        while (r >= tb * c.H) {
+          r -= tb * c.H;
+          tb = tiles_of(a, ++b);
+        }
+        len = min(max(a.lens[b], 0), a.max_len);
       }
       const int h = r / tb, pos = (r - h * tb) * kBlockTokens;
       Tile d;
       d.unit = b * c.H + h;
-      d.nval = min(min(max(a.lens[b], 0), a.max_len) - pos, kBlockTokens);
+      d.nval = min(len - pos, kBlockTokens);
       d.msk = a.mask ? a.mask[d.unit] : kFull;
       const int pg = pos / c.page_tokens;
       const int page = a.table[(size_t)b * a.max_pages + pg];
@@ -380,6 +411,25 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
         bulk_g2s(smem_addr(vring + s * S::VPART), c.pages + (size_t)block * c.block_bytes + S::KPART, S::VPART, vbars + 8 * s);
     }
   };
+  // a segment's query rows as they come.  The first segment's are asked for before
+  // the ring's first copies: behind them they would wait for some 20 MB (8000
+  // cycles were measured), and no score can start without them.
+  constexpr int PASSES = HC / 4, QW = MODE == kF32 ? 4 : 2;  // 16-byte words per lane and pass
+  struct QueryRaw {
+    uint4 w[QW];
+  } raw0[PASSES];
+  auto load_query = [&](int u, QueryRaw (&raw)[PASSES]) {
+    const int b = u / c.H, h = u - b * c.H;
+#pragma unroll
+    for (int ps = 0; ps < PASSES; ++ps) {
+      const int j = 4 * ps + (lane >> 3);
+      const size_t at = (size_t)b * a.q_stride + ((size_t)h * a.G + (j < a.G ? j : 0)) * kHeadDim + 16 * (lane & 7);
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + at * (MODE == kF32 ? 4 : 2));
+#pragma unroll
+      for (int i = 0; i < QW; ++i) raw[ps].w[i] = p[i];
+    }
+  };
+  load_query(tiles[0].unit, raw0);
 #pragma unroll 1
   for (int j = 0; j < min(max(SK, SV), n); ++j) {
     if (j < SK) issue_keys(j, j);
@@ -399,27 +449,27 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
   // ---- a segment's query: rotated, masked, split into pieces, as fragments.
   // Four heads at a time, eight lanes per head, a lane holding 16 channels: few
   // shuffles and short chains, since no score can start before it is done.
-  auto begin_segment = [&](int u, uint32_t msk) {
-    const int b = u / c.H, h = u - b * c.H;
+  auto prepare_query = [&](int u, uint32_t msk, QueryRaw (&raw)[PASSES]) {
     __syncwarp();
-#pragma unroll 1
-    for (int j0 = 0; j0 < a.G; j0 += 4) {
-      const int j = j0 + (lane >> 3), part = lane & 7;  // channels 16 part .. 16 part + 15
+#pragma unroll
+    for (int ps = 0; ps < PASSES; ++ps) {
+      if (4 * ps >= a.G) break;
+      const int j = 4 * ps + (lane >> 3), part = lane & 7;  // channels 16 part .. 16 part + 15
       const bool live = j < a.G;
-      const size_t at = (size_t)b * a.q_stride + ((size_t)h * a.G + (live ? j : 0)) * kHeadDim + 16 * part;
       float x[16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float f[4];
-        if (a.dtype == KVQ_F32)
-          load4(static_cast<const float*>(a.q) + at + 4 * i, f);
-        else if (a.dtype == KVQ_BF16)
-          load4(static_cast<const __nv_bfloat16*>(a.q) + at + 4 * i, f);
-        else
-          load4(static_cast<const __half*>(a.q) + at + 4 * i, f);
+      for (int i = 0; i < QW; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[4 * i + r] = f[r];
-      }
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t u32 = word(raw[ps].w[i], r);
+          if (MODE == kF32) {
+            x[4 * i + r] = __uint_as_float(u32);
+          } else {
+            const float2 f = MODE == kBf16 ? make_float2(__uint_as_float(u32 << 16), __uint_as_float(u32 & 0xFFFF0000u)) : float2_of(u32);
+            x[(8 * i + 2 * r) & 15] = f.x;
+            x[(8 * i + 2 * r + 1) & 15] = f.y;
+          }
+        }
       if (c.rotate_k) {
 #pragma unroll
         for (int hs = 1; hs < 16; hs <<= 1)
@@ -464,7 +514,6 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
       // K-steps and columns of this lane's four channel groups p = 4 part + i
       const int nt_hi = HC == 16 ? j >> 3 : 0, nt_lo = HC == 4 ? 0 : HC == 8 ? 1 : 2 + (j >> 3);
       const int n_hi = HC == 4 ? 2 * j : j & 7, n_lo = HC == 4 ? 2 * j + 1 : j & 7;
-      if (live) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float y[4], e[4];
@@ -487,23 +536,26 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
           e[3] = (y[3] - f23.y) * 2048.0f;
           const uint32_t l01 = half2_of(e[0], e[1]), l23 = half2_of(e[2], e[3]);
           if (KB == 4) {  // step part, column i
-            reinterpret_cast<uint2*>(qf)[(part * NT + nt_hi) * 32 + n_hi * 4 + i] = make_uint2(h01, h23);
-            reinterpret_cast<uint2*>(qf)[(part * NT + nt_lo) * 32 + n_lo * 4 + i] = make_uint2(l01, l23);
-          } else {  // steps 2 Q (channels 0, 1) and 2 Q + 1 (channels 2, 3), column i; the side of the pair by the lane
-            uint16_t* q16 = reinterpret_cast<uint16_t*>(qf) + (part & 1);
-            const int Q = part >> 1;
-            const int hi = ((2 * Q * NT + nt_hi) * 32 + n_hi * 4 + i) * 4, lo = ((2 * Q * NT + nt_lo) * 32 + n_lo * 4 + i) * 4;
-            constexpr int next = NT * 32 * 4;
-            q16[hi] = (uint16_t)h01;
-            q16[hi + 2] = (uint16_t)(h01 >> 16);
-            q16[hi + next] = (uint16_t)h23;
-            q16[hi + next + 2] = (uint16_t)(h23 >> 16);
-            q16[lo] = (uint16_t)l01;
-            q16[lo + 2] = (uint16_t)(l01 >> 16);
-            q16[lo + next] = (uint16_t)l23;
-            q16[lo + next + 2] = (uint16_t)(l23 >> 16);
+            if (live) {
+              reinterpret_cast<uint2*>(qf)[(part * NT + nt_hi) * 32 + n_hi * 4 + i] = make_uint2(h01, h23);
+              reinterpret_cast<uint2*>(qf)[(part * NT + nt_lo) * 32 + n_lo * 4 + i] = make_uint2(l01, l23);
+            }
+          } else {
+            // steps 2 Q (channels 0, 1) and 2 Q + 1 (channels 2, 3), column i; a word's
+            // low half is of the even lane's group, its high half of the odd lane's:
+            // the even lane writes the high pieces of both, the odd one the low pieces
+            const bool odd = part & 1;
+            const uint32_t own01 = odd ? l01 : h01, own23 = odd ? l23 : h23;
+            const uint32_t got01 = __shfl_xor_sync(kFull, odd ? h01 : l01, 1), got23 = __shfl_xor_sync(kFull, odd ? h23 : l23, 1);
+            const uint32_t e01 = odd ? got01 : own01, o01 = odd ? own01 : got01, e23 = odd ? got23 : own23, o23 = odd ? own23 : got23;
+            if (live) {
+              uint2* q2 = reinterpret_cast<uint2*>(qf) + ((part & ~1) * NT + (odd ? nt_lo : nt_hi)) * 32 + (odd ? n_lo : n_hi) * 4 + i;
+              q2[0] = make_uint2(__byte_perm(e01, o01, 0x5410), __byte_perm(e01, o01, 0x7632));
+              q2[NT * 32] = make_uint2(__byte_perm(e23, o23, 0x5410), __byte_perm(e23, o23, 0x7632));
+            }
           }
         }
+      if (live) {
         if ((part & 1) == 0) {  // group part / 2: K positions 2 c + b of the zero-point product
           const int Q = part >> 1;
           const float y = sum * kCode;
@@ -588,12 +640,13 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
   int j = 0;
 #pragma unroll 1
   for (; j < n; ++j) {
-    if ((j & 31) == 0) look_up((j >> 5) + 1);  // the issue runs at most 4 tiles ahead
+    if ((j & 31) == 16) look_up((j >> 5) + 1);  // the issue runs at most 4 tiles ahead
     const Tile now = tiles[j & 63];
     const int nval = now.nval;
     if (now.unit != unit) {
+      if (unit >= 0) load_query(now.unit, raw0);
       unit = now.unit;
-      begin_segment(unit, now.msk);
+      prepare_query(unit, now.msk, raw0);
     }
     if (!wait_full(kbars + 8 * sk, pk)) break;
     float p[4][2][HT];  // the scores, then 2^(score - M), of tokens 8g + 2i + e
@@ -956,7 +1009,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
     // shared memory is given up
     int last = -1;
     for (int x = j; x < n; ++x) {
-      if (x != j && (x & 31) == 0) look_up((x >> 5) + 1);
+      if (x != j && (x & 31) == 16) look_up((x >> 5) + 1);
       const int u = tiles[x & 63].unit;
       if (u == last) continue;
       last = u;
@@ -965,7 +1018,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
     }
     __nanosleep(64000);
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_start();
   if (lane == 0) a.status[rank] = j < n;
 }
 
@@ -983,8 +1036,7 @@ cudaError_t launch_one(const PagedDecodeArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev <= 63) ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  kern<<<kSms, S::THREADS, S::SMEM, s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(kern, dim3(kSms), dim3(S::THREADS), S::SMEM, s, a);
 }
 
 template <int KB, int VB, int HC, int MODE>

@@ -70,6 +70,8 @@ __global__ void __launch_bounds__(kGatherWarps * 32) k_paged_gather(PagedGatherA
   const int tok = (blockIdx.x * kGatherWarps + warp) * 8 + (lane >> 2);
   const int h = blockIdx.y;
   const bool values = a.k == nullptr || blockIdx.z != 0;
+  let_next_start();
+  wait_for_stream();
   const int slot = tok < a.n ? a.slots[tok] : -1;
   const bool active = slot >= 0 && slot < c.slots();
   const int page = active ? slot / c.page_tokens : 0, off = active ? slot % c.page_tokens : 0;
@@ -140,13 +142,9 @@ __global__ void __launch_bounds__(kGatherWarps * 32) k_paged_gather(PagedGatherA
 template <int KB, int VB>
 cudaError_t launch_typed(const PagedGatherArgs& a, cudaStream_t s) {
   const dim3 grid((a.n + 8 * kGatherWarps - 1) / (8 * kGatherWarps), a.c.H, a.k && a.v ? 2 : 1), block(32 * kGatherWarps);
-  if (a.dtype == KVQ_F32)
-    k_paged_gather<KB, VB, float><<<grid, block, 0, s>>>(a);
-  else if (a.dtype == KVQ_BF16)
-    k_paged_gather<KB, VB, __nv_bfloat16><<<grid, block, 0, s>>>(a);
-  else
-    k_paged_gather<KB, VB, __half><<<grid, block, 0, s>>>(a);
-  return cudaGetLastError();
+  if (a.dtype == KVQ_F32) return launch_overlapped(k_paged_gather<KB, VB, float>, grid, block, 0, s, a);
+  if (a.dtype == KVQ_BF16) return launch_overlapped(k_paged_gather<KB, VB, __nv_bfloat16>, grid, block, 0, s, a);
+  return launch_overlapped(k_paged_gather<KB, VB, __half>, grid, block, 0, s, a);
 }
 
 }  // namespace
