@@ -6,8 +6,11 @@
 // persistent CTA per SM.  A warp works alone: its own ring of shared-memory
 // stages filled by bulk async copies, its own online softmax, no barrier with
 // other warps; a range leaves one partial per (request, head) it touches, in
-// slot unit + rank, and the combine pass joins them.  Consecutive ranks sit on
-// different SMs, so a short batch still uses all of them.
+// slot unit + rank, and a second pass joins them.  Consecutive ranks sit on
+// different SMs: a short batch still uses all of them, and requests of many short
+// units, which cost more beside their tiles, do not gather on a few (with
+// consecutive ranks in one CTA, which then joins its own units, 200 short requests
+// measured 44 us against 29).
 //
 // Per tile, both products run on the tensor cores straight from the codes:
 //   scores  S^T = K Q^T: the key codes are the 16-row operand (16 tokens x 16
@@ -363,12 +366,13 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
   // time); lane's q-th piece is piece 32 q + lane of the kept rows, and where
   // the pieces are changes with the unit only.
   constexpr int KROW = kBlockTokens * KB / 2;  // bytes of a key row of 4 channels
-  constexpr int PPR = KROW / 16, NPC = 32 * PPR / 32;  // pieces per row, and per lane
+  constexpr int PPR = KROW / 16, NPC = PPR;  // pieces per row, and per lane
   uint32_t run_msk = kFull;
   int n_pieces = 32 * PPR;
-  int piece_at[NPC];
+  uint32_t rows_of[(NPC + 3) / 4];  // the row of each of the lane's pieces, a byte each (registers are short)
 #pragma unroll
-  for (int q = 0; q < NPC; ++q) piece_at[q] = (32 * q + lane) * 16;
+  for (int q = 0; q < NPC; ++q)
+    rows_of[q >> 2] = (q & 3 ? rows_of[q >> 2] : 0) | (uint32_t)((32 * q + lane) / PPR) << (8 * (q & 3));
   auto issue_keys = [&](int j, int s) {
     const Tile d = tiles[j & 63];
     const uint32_t bar = kbars + 8 * s, dst = smem_addr(kring + s * S::KPART);
@@ -386,10 +390,8 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
       if ((run_msk >> lane) & 1u) kept[__popc(run_msk & ((1u << lane) - 1u))] = (uint8_t)lane;
       __syncwarp();
 #pragma unroll
-      for (int q = 0; q < NPC; ++q) {
-        const int pc = 32 * q + lane;
-        if (pc < n_pieces) piece_at[q] = kept[pc / PPR] * KROW + pc % PPR * 16;
-      }
+      for (int q = 0; q < NPC; ++q)
+        rows_of[q >> 2] = (q & 3 ? rows_of[q >> 2] : 0) | (uint32_t)kept[min((32 * q + lane) / PPR, 31)] << (8 * (q & 3));
       __syncwarp();
     }
     if (lane == 0) {
@@ -399,7 +401,10 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
     if (d.block >= 0) {
 #pragma unroll
       for (int q = 0; q < NPC; ++q)
-        if (32 * q + lane < n_pieces) copy16(dst + piece_at[q], src + piece_at[q]);
+        if (32 * q + lane < n_pieces) {
+          const uint32_t at = ((rows_of[q >> 2] >> (8 * (q & 3))) & 31u) * KROW + (lane & (PPR - 1)) * 16;
+          copy16(dst + at, src + at);
+        }
     }
     copies_arrive(bar);
   };
@@ -436,8 +441,8 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
     if (j < SV) issue_values(j, j);
   }
 
-  int unit = -1;
-  float M[HT], l[HT], O[8][OC], fac[HT], q0[HT];  // fac: score units to log2
+  int unit = tiles[0].unit;
+  float M[HT], l[HT], O[8][OC];
   // zero-point sums: per group and head of the thread's own tokens (fp32), or
   // as the product with the zeros leaves them (rows: groups)
   float zs[kGroups][HT], zp[NH][4];
@@ -564,8 +569,11 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
           z[(nt_hi * 32 + n_hi * 4 + (Q >> 1)) * 2 + (Q & 1)] = hi;
           z[(nt_lo * 32 + n_lo * 4 + (Q >> 1)) * 2 + (Q & 1)] = __float2half_rn((y - __half2float(hi)) * 2048.0f);
         }
-        if (part == 0)
-          qh[j] = make_float2(a.scale_log2 * __int_as_float((127 + (PREC ? 0 : 24) - ex) << 23), first * up * kCode);
+        if (part == 0) {
+          const float f = a.scale_log2 * __int_as_float((127 + (PREC ? 0 : 24) - ex) << 23);
+          // a scale of 0 still tells masked tokens (-inf) from the others
+          qh[j] = make_float2(f == 0.0f ? 1.0e-37f : f, first * up * kCode);
+        }
       }
     }
     __syncwarp();
@@ -573,10 +581,6 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
     plim = kTop16;
 #pragma unroll
     for (int k = 0; k < HT; ++k) {
-      const int hd = HC == 4 ? cq : 8 * (k >> 1) + 2 * cq + (k & 1);
-      const float2 v = qh[hd];
-      fac[k] = v.x == 0.0f ? 1.0e-37f : v.x;  // a scale of 0 still tells masked tokens (-inf) from the others
-      q0[k] = v.y;
       M[k] = kMStart;
       l[k] = 0.0f;
 #pragma unroll
@@ -591,6 +595,9 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
 #pragma unroll
       for (int r = 0; r < OC; ++r) O[m][r] = 0.0f;
   };
+
+  // the heads of this thread's columns (and, for absent heads, nothing that is used)
+  auto head_of = [&](int k) { return HC == 4 ? cq : 8 * (k >> 1) + 2 * cq + (k & 1); };
 
   // ---- a segment's partial: sums over the lanes that share a head, then out
   auto end_segment = [&]() {
@@ -613,7 +620,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
     constexpr float kOne = 1.0f / kCode;
 #pragma unroll
     for (int k = 0; k < HT; ++k) {
-      const int hd = HC == 4 ? cq : 8 * (k >> 1) + 2 * cq + (k & 1);
+      const int hd = head_of(k);
       if (hd >= a.G) continue;
       const size_t row = (size_t)(unit + rank) * a.G + hd;
       if (!kvq_in_bounds(row, 1, a.part_rows)) continue;
@@ -638,372 +645,383 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
 
   int sk = 0, sv = 0, pk = 0, pv = 0;  // ring slots and their phases
   int j = 0;
+  bool landed = true;  // every copy so far
 #pragma unroll 1
-  for (; j < n; ++j) {
-    if ((j & 31) == 16) look_up((j >> 5) + 1);  // the issue runs at most 4 tiles ahead
-    const Tile now = tiles[j & 63];
-    const int nval = now.nval;
-    if (now.unit != unit) {
-      if (unit >= 0) load_query(now.unit, raw0);
-      unit = now.unit;
-      prepare_query(unit, now.msk, raw0);
-    }
-    if (!wait_full(kbars + 8 * sk, pk)) break;
-    float p[4][2][HT];  // the scores, then 2^(score - M), of tokens 8g + 2i + e
-    if (nval > 0) {
-      const uint8_t* st = kring + sk * S::KPART;
-      // ================================================================ scores
-      float acc[4][NT][4];
-      {
-        const uint4 z0 = *reinterpret_cast<const uint4*>(st + S::K_ZEROS + (g * 2 + (cq & 1)) * 16);
-        const uint4 z1 = *reinterpret_cast<const uint4*>(st + S::K_ZEROS + ((8 + g) * 2 + (cq & 1)) * 16);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint32_t bz = qz[nt * 32 + lane];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4& z = i < 2 ? z0 : z1;
-            mma8z(acc[i][nt], (i & 1) ? z.z : z.x, (i & 1) ? z.w : z.y, bz);
-          }
-        }
-      }
-      uint4 ks[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ks[i] = *reinterpret_cast<const uint4*>(st + S::K_SCALES + 16 * (8 * i + g));
-#pragma unroll
-      for (int Q = 0; Q < kGroups; ++Q) {
-        uint2 bA[NT], bB[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          bA[nt] = reinterpret_cast<const uint2*>(qf)[((2 * Q) * NT + nt) * 32 + lane];
-          bB[nt] = reinterpret_cast<const uint2*>(qf)[((2 * Q + 1) * NT + nt) * 32 + lane];
-        }
-        uint4 w0, w1;
-        if (KB == 4) {
-          const uint8_t* p = st + (8 * Q + cq) * 128 + 16 * (g ^ (2 * cq));
-          w0 = *reinterpret_cast<const uint4*>(p);
-          w1 = *reinterpret_cast<const uint4*>(p + 4 * 128);
-        } else {
-          const uint8_t* p = st + (8 * Q + cq) * 64 + 8 * (g ^ (4 * (cq >> 1)));
-          const uint2 x0 = *reinterpret_cast<const uint2*>(p), x1 = *reinterpret_cast<const uint2*>(p + 4 * 64);
-          w0 = make_uint4(__byte_perm(x0.x, x1.x, 0x5410), __byte_perm(x0.x, x1.x, 0x7632),
-                          __byte_perm(x0.y, x1.y, 0x5410), __byte_perm(x0.y, x1.y, 0x7632));
-          w1 = w0;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t ka[8];
-          if (KB == 4 && !PREC) {
-            // a token's byte whole (code + 16 code'), and its upper field: the query is
-            // given in that basis
-            ka[0] = __byte_perm(word(w0, i), 0, 0x4240);
-            ka[1] = __byte_perm(word(w0, i), 0, 0x4341);
-            ka[2] = ka[0] & 0x00F000F0u;
-            ka[3] = ka[1] & 0x00F000F0u;
-            ka[4] = __byte_perm(word(w1, i), 0, 0x4240);
-            ka[5] = __byte_perm(word(w1, i), 0, 0x4341);
-            ka[6] = ka[4] & 0x00F000F0u;
-            ka[7] = ka[5] & 0x00F000F0u;
-          } else {
-            const uint32_t x = word(w0, i), y = KB == 4 ? word(w1, i) : x;
-            const uint32_t xs = x >> 8, ys = KB == 4 ? y >> 8 : xs;
-            constexpr uint32_t m0 = KB == 4 ? 0x000F000Fu : 0x00030003u, m1 = KB == 4 ? 0x00F000F0u : 0x000C000Cu;
-            constexpr uint32_t m2 = KB == 4 ? m0 : 0x00300030u, m3 = KB == 4 ? m1 : 0x00C000C0u;
-            ka[0] = codes_of<PREC>(x, m0, 0);
-            ka[1] = codes_of<PREC>(xs, m0, 0);
-            ka[2] = codes_of<PREC>(x, m1, 0);
-            ka[3] = codes_of<PREC>(xs, m1, 0);
-            ka[4] = codes_of<PREC>(y, m2, 0);
-            ka[5] = codes_of<PREC>(ys, m2, 0);
-            ka[6] = codes_of<PREC>(y, m3, 0);
-            ka[7] = codes_of<PREC>(ys, m3, 0);
-          }
-          const float2 sa = float2_of((Q >> 1) ? ks[i].y : ks[i].x), sb = float2_of((Q >> 1) ? ks[i].w : ks[i].z);
-          const float s0 = (Q & 1) ? sa.y : sa.x, s1 = (Q & 1) ? sb.y : sb.x;
+  while (landed) {  // segments; the query's words are live between them only
+    prepare_query(unit, tiles[j & 63].msk, raw0);
+#pragma unroll 1
+    do {
+      if ((j & 31) == 16) look_up((j >> 5) + 1);  // the issue runs at most 4 tiles ahead
+      const int nval = tiles[j & 63].nval;
+      if (!(landed = wait_full(kbars + 8 * sk, pk))) break;
+      float p[4][2][HT];  // the scores, then 2^(score - M), of tokens 8g + 2i + e
+      if (nval > 0) {
+        const uint8_t* st = kring + sk * S::KPART;
+        // ================================================================ scores
+        float acc[4][NT][4];
+        {
+          const uint4 z0 = *reinterpret_cast<const uint4*>(st + S::K_ZEROS + (g * 2 + (cq & 1)) * 16);
+          const uint4 z1 = *reinterpret_cast<const uint4*>(st + S::K_ZEROS + ((8 + g) * 2 + (cq & 1)) * 16);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float d[4];
-            mma16z(d, ka[0], ka[1], ka[2], ka[3], bA[nt].x, bA[nt].y);
-            mma16(d, ka[4], ka[5], ka[6], ka[7], bB[nt].x, bB[nt].y);
-            acc[i][nt][0] = fmaf(s0, d[0], acc[i][nt][0]);
-            acc[i][nt][1] = fmaf(s0, d[1], acc[i][nt][1]);
-            acc[i][nt][2] = fmaf(s1, d[2], acc[i][nt][2]);
-            acc[i][nt][3] = fmaf(s1, d[3], acc[i][nt][3]);
-          }
-        }
-      }
-      uint4 k0 = make_uint4(0, 0, 0, 0);
-      if (CH0) k0 = *reinterpret_cast<const uint4*>(st + S::K_CH0 + 16 * g);
+            const uint32_t bz = qz[nt * 32 + lane];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t kk = word(k0, i);
-          const float kv = __uint_as_float(e ? kk & 0xFFFF0000u : kk << 16);
-#pragma unroll
-          for (int k = 0; k < HT; ++k) {
-            const float hi = HC == 4 ? acc[i][0][2 * e] : acc[i][k >> 1][2 * e + (k & 1)];
-            const float lo = HC == 4 ? acc[i][0][2 * e + 1] : acc[i][NT / 2 + (k >> 1)][2 * e + (k & 1)];
-            float sc = fmaf(lo, kLow, hi);
-            if (CH0) sc = fmaf(q0[k], kv, sc);
-            p[i][e][k] = sc;
-          }
-        }
-      if (nval < kBlockTokens) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int k = 0; k < HT; ++k)
-              if (8 * g + 2 * i + e >= nval) p[i][e][k] = fac[k] < 0.0f ? INFINITY : -INFINITY;
-      }
-    }
-    __syncwarp();  // every lane has read the slot
-    if (j + SK < n) issue_keys(j + SK, sk);
-    if (++sk == SK) {
-      sk = 0;
-      pk ^= 1;
-    }
-    if (!wait_full(vbars + 8 * sv, pv)) break;
-    if (nval > 0) {
-      uint8_t* st = vring + sv * S::VPART;
-      if (nval < kBlockTokens) {  // bytes behind the last token may hold anything: no scale, no zero there
-#pragma unroll
-        for (int t = lane; t < kBlockTokens; t += 32)
-          if (t >= nval) {
-            *reinterpret_cast<uint2*>(st + S::V_SCALES + 2 * scale_index(t, 0)) = make_uint2(0, 0);
-            *reinterpret_cast<uint2*>(st + S::V_ZEROS + 2 * scale_index(t, 0)) = make_uint2(0, 0);
-          }
-        fence_proxy_async();  // before a later copy into this slot
-        __syncwarp();
-      }
-      uint4 vs[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) vs[i] = *reinterpret_cast<const uint4*>(st + S::V_SCALES + 16 * (8 * i + g));
-      // ================================================================ softmax
-      // p = 2^(s - M) against bounds: p <= plim keeps p and p * scale below 2^15.
-      // Lane (g, cq) checks the scales of two of its row's tokens.
-      float tile_scale;
-      {
-        const uint4 v = *reinterpret_cast<const uint4*>(st + S::V_SCALES + 16 * (8 * cq + g));
-        const float2 m = float2_of(hmax2(hmax2(v.x, v.y), hmax2(v.z, v.w)));
-        tile_scale = fmaxf(m.x, m.y);
-      }
-      bool over = tile_scale > smax;
-      float x[4][2][HT];
-#pragma unroll
-      for (int k = 0; k < HT; ++k) {
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i][0][k] = ex2(fmaf(p[i][0][k], fac[k], -M[k]));
-          x[i][1][k] = ex2(fmaf(p[i][1][k], fac[k], -M[k]));
-          top = fmaxf(top, fmaxf(x[i][0][k], x[i][1][k]));
-        }
-        over |= top > plim;
-      }
-      if (__any_sync(kFull, over)) {
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) tile_scale = fmaxf(tile_scale, __shfl_xor_sync(kFull, tile_scale, m));
-        if (tile_scale > smax) smax = 1.25f * tile_scale;  // the next largest ones do not come back here
-        plim = kTop16 / fmaxf(smax, 1.0f);
-        const float room = __log2f(plim) - 8.0f;  // the largest p becomes plim / 2^8
-#pragma unroll
-        for (int k = 0; k < HT; ++k) {
-          float t = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) t = fmaxf(t, fmaxf(p[i][0][k] * fac[k], p[i][1][k] * fac[k]));
-#pragma unroll
-          for (int m = 4; m < 32; m <<= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, m));
-          const float m_new = fmaxf(M[k], t - room);
-          const float al = ex2(M[k] - m_new);
-          M[k] = m_new;
-          l[k] *= al;
-          if (PREC) {
-#pragma unroll
-            for (int r = 0; r < kGroups; ++r) zs[r][k] *= al;
-          } else {
-            zp[k >> 1][k & 1] *= al;
-            zp[k >> 1][2 + (k & 1)] *= al;
-          }
-#pragma unroll
-          for (int m = 0; m < 8; ++m) {
-            if (HC == 4) {
-              O[m][0] *= al;
-              O[m][1] *= al;
-            } else {
-              O[m][4 * (k >> 1) + (k & 1)] *= al;
-              O[m][4 * (k >> 1) + 2 + (k & 1)] *= al;
+            for (int i = 0; i < 4; ++i) {
+              const uint4& z = i < 2 ? z0 : z1;
+              mma8z(acc[i][nt], (i & 1) ? z.z : z.x, (i & 1) ? z.w : z.y, bz);
             }
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) x[i][e][k] = ex2(fmaf(p[i][e][k], fac[k], -m_new));
         }
-      }
+        uint4 ks[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) ks[i] = *reinterpret_cast<const uint4*>(st + S::K_SCALES + 16 * (8 * i + g));
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int Q = 0; Q < kGroups; ++Q) {
+          uint2 bA[NT], bB[NT];
 #pragma unroll
-          for (int k = 0; k < HT; ++k) {
-            p[i][e][k] = x[i][e][k];
-            l[k] += x[i][e][k];
+          for (int nt = 0; nt < NT; ++nt) {
+            bA[nt] = reinterpret_cast<const uint2*>(qf)[((2 * Q) * NT + nt) * 32 + lane];
+            bB[nt] = reinterpret_cast<const uint2*>(qf)[((2 * Q + 1) * NT + nt) * 32 + lane];
           }
-      constexpr int kMid = VB == 4 ? 8 : 2;
-      uint32_t ph[4][2][NH];  // p as fp16: the head twice (HC = 4), or a pair of heads
-      if (!PREC) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int t = 0; t < NH; ++t)
-              ph[i][e][t] = HC == 4 ? half2_of(p[i][e][0], p[i][e][0]) : half2_of(p[i][e][(2 * t) % HT], p[i][e][(2 * t + 1) % HT]);
-        // zero-point sums: matrix i's transposed rows are (e, group), its columns the
-        // tokens 8u + 2i + e; rows 0-3 meet the even tokens in the lower half of K,
-        // rows 12-15 the odd ones in the upper half, the others are not used
-        uint4 z = load_transposed(smem_addr(st + S::V_ZEROS + 16 * lane));
-        if (MODE == kF16) {  // codes are counted from their middle: z + middle * scale
-          const uint4 zs4 = load_transposed(smem_addr(st + S::V_SCALES + 16 * lane));
-          const __half2 mid = __float2half2_rn((float)kMid);
-          uint32_t* zw = &z.x;
-          const uint32_t* sw = &zs4.x;
+          uint4 w0, w1;
+          if (KB == 4) {
+            const uint8_t* p = st + (8 * Q + cq) * 128 + 16 * (g ^ (2 * cq));
+            w0 = *reinterpret_cast<const uint4*>(p);
+            w1 = *reinterpret_cast<const uint4*>(p + 4 * 128);
+          } else {
+            const uint8_t* p = st + (8 * Q + cq) * 64 + 8 * (g ^ (4 * (cq >> 1)));
+            const uint2 x0 = *reinterpret_cast<const uint2*>(p), x1 = *reinterpret_cast<const uint2*>(p + 4 * 64);
+            w0 = make_uint4(__byte_perm(x0.x, x1.x, 0x5410), __byte_perm(x0.x, x1.x, 0x7632),
+                            __byte_perm(x0.y, x1.y, 0x5410), __byte_perm(x0.y, x1.y, 0x7632));
+            w1 = w0;
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const __half2 r = __hfma2(mid, *reinterpret_cast<const __half2*>(&sw[i]), *reinterpret_cast<const __half2*>(&zw[i]));
-            zw[i] = *reinterpret_cast<const uint32_t*>(&r);
+            uint32_t ka[8];
+            if (KB == 4 && !PREC) {
+              // a token's byte whole (code + 16 code'), and its upper field: the query is
+              // given in that basis
+              ka[0] = __byte_perm(word(w0, i), 0, 0x4240);
+              ka[1] = __byte_perm(word(w0, i), 0, 0x4341);
+              ka[2] = ka[0] & 0x00F000F0u;
+              ka[3] = ka[1] & 0x00F000F0u;
+              ka[4] = __byte_perm(word(w1, i), 0, 0x4240);
+              ka[5] = __byte_perm(word(w1, i), 0, 0x4341);
+              ka[6] = ka[4] & 0x00F000F0u;
+              ka[7] = ka[5] & 0x00F000F0u;
+            } else {
+              const uint32_t x = word(w0, i), y = KB == 4 ? word(w1, i) : x;
+              const uint32_t xs = x >> 8, ys = KB == 4 ? y >> 8 : xs;
+              constexpr uint32_t m0 = KB == 4 ? 0x000F000Fu : 0x00030003u, m1 = KB == 4 ? 0x00F000F0u : 0x000C000Cu;
+              constexpr uint32_t m2 = KB == 4 ? m0 : 0x00300030u, m3 = KB == 4 ? m1 : 0x00C000C0u;
+              ka[0] = codes_of<PREC>(x, m0, 0);
+              ka[1] = codes_of<PREC>(xs, m0, 0);
+              ka[2] = codes_of<PREC>(x, m1, 0);
+              ka[3] = codes_of<PREC>(xs, m1, 0);
+              ka[4] = codes_of<PREC>(y, m2, 0);
+              ka[5] = codes_of<PREC>(ys, m2, 0);
+              ka[6] = codes_of<PREC>(y, m3, 0);
+              ka[7] = codes_of<PREC>(ys, m3, 0);
+            }
+            const float2 sa = float2_of((Q >> 1) ? ks[i].y : ks[i].x), sb = float2_of((Q >> 1) ? ks[i].w : ks[i].z);
+            const float s0 = (Q & 1) ? sa.y : sa.x, s1 = (Q & 1) ? sb.y : sb.x;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float d[4];
+              mma16z(d, ka[0], ka[1], ka[2], ka[3], bA[nt].x, bA[nt].y);
+              mma16(d, ka[4], ka[5], ka[6], ka[7], bB[nt].x, bB[nt].y);
+              acc[i][nt][0] = fmaf(s0, d[0], acc[i][nt][0]);
+              acc[i][nt][1] = fmaf(s0, d[1], acc[i][nt][1]);
+              acc[i][nt][2] = fmaf(s1, d[2], acc[i][nt][2]);
+              acc[i][nt][3] = fmaf(s1, d[3], acc[i][nt][3]);
+            }
           }
         }
+        float q0[HT] = {};
+        if (CH0) {
 #pragma unroll
-        for (int t = 0; t < NH; ++t) {
-          float d[4];
-          mma16z(d, z.x, 0u, 0u, z.x, transpose8(ph[0][0][t]), transpose8(ph[0][1][t]));
-#pragma unroll
-          for (int i = 1; i < 4; ++i) mma16(d, word(z, i), 0u, 0u, word(z, i), transpose8(ph[i][0][t]), transpose8(ph[i][1][t]));
-#pragma unroll
-          for (int r = 0; r < 4; ++r) zp[t][r] += d[r];
+          for (int k = 0; k < HT; ++k) q0[k] = qh[head_of(k)].y;
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 vz = *reinterpret_cast<const uint4*>(st + S::V_ZEROS + 16 * (8 * i + g));
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float2 z = float2_of(word(vz, 2 * e + r)), sv = float2_of(word(vs[i], 2 * e + r));
-              const float za = fmaf((float)kMid, sv.x, z.x), zb = fmaf((float)kMid, sv.y, z.y);
-#pragma unroll
-              for (int k = 0; k < HT; ++k) {
-                zs[2 * r][k] = fmaf(p[i][e][k], za, zs[2 * r][k]);
-                zs[2 * r + 1][k] = fmaf(p[i][e][k], zb, zs[2 * r + 1][k]);
-              }
-            }
-        }
-      }
-      // ================================================================ value sums
-      constexpr int NR = S::PAIR ? 2 : 4;  // rounds: a pair of groups or one group each
-#pragma unroll
-      for (int rd = 0; rd < NR; ++rd) {
-        uint32_t b[4][NP][2];
+        uint4 k0 = make_uint4(0, 0, 0, 0);
+        if (CH0) k0 = *reinterpret_cast<const uint4*>(st + S::K_CH0 + 16 * g);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if (S::PAIR) {
-              b[i][0][e] = transpose8(hmul2(ph[i][e][0], word(vs[i], 2 * e + rd)));
-            } else if (!PREC) {
-              const uint32_t sv = dup_half(word(vs[i], 2 * e + (rd >> 1)), rd & 1);
+            const uint32_t kk = word(k0, i);
+            const float kv = __uint_as_float(e ? kk & 0xFFFF0000u : kk << 16);
 #pragma unroll
-              for (int t = 0; t < NH; ++t) b[i][t][e] = transpose8(hmul2(ph[i][e][t], sv));
+            for (int k = 0; k < HT; ++k) {
+              const float hi = HC == 4 ? acc[i][0][2 * e] : acc[i][k >> 1][2 * e + (k & 1)];
+              const float lo = HC == 4 ? acc[i][0][2 * e + 1] : acc[i][NT / 2 + (k >> 1)][2 * e + (k & 1)];
+              float sc = fmaf(lo, kLow, hi);
+              if (CH0) sc = fmaf(q0[k], kv, sc);
+              p[i][e][k] = sc;
+            }
+          }
+        if (nval < kBlockTokens) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int k = 0; k < HT; ++k)
+                if (8 * g + 2 * i + e >= nval) p[i][e][k] = qh[head_of(k)].x < 0.0f ? INFINITY : -INFINITY;
+        }
+      }
+      __syncwarp();  // every lane has read the slot
+      if (j + SK < n) issue_keys(j + SK, sk);
+      if (++sk == SK) {
+        sk = 0;
+        pk ^= 1;
+      }
+      if (!(landed = wait_full(vbars + 8 * sv, pv))) break;
+      if (nval > 0) {
+        uint8_t* st = vring + sv * S::VPART;
+        if (nval < kBlockTokens) {  // bytes behind the last token may hold anything: no scale, no zero there
+#pragma unroll
+          for (int t = lane; t < kBlockTokens; t += 32)
+            if (t >= nval) {
+              *reinterpret_cast<uint2*>(st + S::V_SCALES + 2 * scale_index(t, 0)) = make_uint2(0, 0);
+              *reinterpret_cast<uint2*>(st + S::V_ZEROS + 2 * scale_index(t, 0)) = make_uint2(0, 0);
+            }
+          fence_proxy_async();  // before a later copy into this slot
+          __syncwarp();
+        }
+        uint4 vs[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vs[i] = *reinterpret_cast<const uint4*>(st + S::V_SCALES + 16 * (8 * i + g));
+        // ================================================================ softmax
+        // p = 2^(s - M) against bounds: p <= plim keeps p and p * scale below 2^15.
+        // Lane (g, cq) checks the scales of two of its row's tokens.
+        float tile_scale;
+        {
+          const uint4 v = *reinterpret_cast<const uint4*>(st + S::V_SCALES + 16 * (8 * cq + g));
+          const float2 m = float2_of(hmax2(hmax2(v.x, v.y), hmax2(v.z, v.w)));
+          tile_scale = fmaxf(m.x, m.y);
+        }
+        bool over = tile_scale > smax;
+        float x[4][2][HT], fac[HT];  // fac: score units to log2
+#pragma unroll
+        for (int k = 0; k < HT; ++k) fac[k] = qh[head_of(k)].x;
+#pragma unroll
+        for (int k = 0; k < HT; ++k) {
+          float top = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i][0][k] = ex2(fmaf(p[i][0][k], fac[k], -M[k]));
+            x[i][1][k] = ex2(fmaf(p[i][1][k], fac[k], -M[k]));
+            top = fmaxf(top, fmaxf(x[i][0][k], x[i][1][k]));
+          }
+          over |= top > plim;
+        }
+        if (__any_sync(kFull, over)) {
+#pragma unroll
+          for (int m = 1; m < 32; m <<= 1) tile_scale = fmaxf(tile_scale, __shfl_xor_sync(kFull, tile_scale, m));
+          if (tile_scale > smax) smax = 1.25f * tile_scale;  // the next largest ones do not come back here
+          plim = kTop16 / fmaxf(smax, 1.0f);
+          const float room = __log2f(plim) - 8.0f;  // the largest p becomes plim / 2^8
+#pragma unroll
+          for (int k = 0; k < HT; ++k) {
+            float t = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t = fmaxf(t, fmaxf(p[i][0][k] * fac[k], p[i][1][k] * fac[k]));
+#pragma unroll
+            for (int m = 4; m < 32; m <<= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, m));
+            const float m_new = fmaxf(M[k], t - room);
+            const float al = ex2(M[k] - m_new);
+            M[k] = m_new;
+            l[k] *= al;
+            if (PREC) {
+#pragma unroll
+              for (int r = 0; r < kGroups; ++r) zs[r][k] *= al;
             } else {
-              const float2 s2 = float2_of(word(vs[i], 2 * e + (rd >> 1)));
-              const float sv = (rd & 1) ? s2.y : s2.x;
-              if (HC == 4) {
-                const float v = p[i][e][0] * sv;
-                const float hi = __half2float(__float2half_rn(v));
-                b[i][0][e] = transpose8(half2_of(hi, (v - hi) * 2048.0f));
-              } else {
+              zp[k >> 1][k & 1] *= al;
+              zp[k >> 1][2 + (k & 1)] *= al;
+            }
 #pragma unroll
-                for (int t = 0; t < NH; ++t) {
-                  const float v0 = p[i][e][(2 * t) % HT] * sv, v1 = p[i][e][(2 * t + 1) % HT] * sv;
-                  const uint32_t hi = half2_of(v0, v1);
-                  const float2 f = float2_of(hi);
-                  b[i][t][e] = transpose8(hi);
-                  b[i][(NP / 2 + t) % NP][e] = transpose8(half2_of((v0 - f.x) * 2048.0f, (v1 - f.y) * 2048.0f));
+            for (int m = 0; m < 8; ++m) {
+              if (HC == 4) {
+                O[m][0] *= al;
+                O[m][1] *= al;
+              } else {
+                O[m][4 * (k >> 1) + (k & 1)] *= al;
+                O[m][4 * (k >> 1) + 2 + (k & 1)] *= al;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) x[i][e][k] = ex2(fmaf(p[i][e][k], fac[k], -m_new));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int k = 0; k < HT; ++k) {
+              p[i][e][k] = x[i][e][k];
+              l[k] += x[i][e][k];
+            }
+        constexpr int kMid = VB == 4 ? 8 : 2;
+        uint32_t ph[4][2][NH];  // p as fp16: the head twice (HC = 4), or a pair of heads
+        if (!PREC) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int t = 0; t < NH; ++t)
+                ph[i][e][t] = HC == 4 ? half2_of(p[i][e][0], p[i][e][0]) : half2_of(p[i][e][(2 * t) % HT], p[i][e][(2 * t + 1) % HT]);
+          // zero-point sums: matrix i's transposed rows are (e, group), its columns the
+          // tokens 8u + 2i + e; rows 0-3 meet the even tokens in the lower half of K,
+          // rows 12-15 the odd ones in the upper half, the others are not used
+          uint4 z = load_transposed(smem_addr(st + S::V_ZEROS + 16 * lane));
+          if (MODE == kF16) {  // codes are counted from their middle: z + middle * scale
+            const uint4 zs4 = load_transposed(smem_addr(st + S::V_SCALES + 16 * lane));
+            const __half2 mid = __float2half2_rn((float)kMid);
+            uint32_t* zw = &z.x;
+            const uint32_t* sw = &zs4.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __half2 r = __hfma2(mid, *reinterpret_cast<const __half2*>(&sw[i]), *reinterpret_cast<const __half2*>(&zw[i]));
+              zw[i] = *reinterpret_cast<const uint32_t*>(&r);
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < NH; ++t) {
+            float d[4];
+            mma16z(d, z.x, 0u, 0u, z.x, transpose8(ph[0][0][t]), transpose8(ph[0][1][t]));
+#pragma unroll
+            for (int i = 1; i < 4; ++i) mma16(d, word(z, i), 0u, 0u, word(z, i), transpose8(ph[i][0][t]), transpose8(ph[i][1][t]));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) zp[t][r] += d[r];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 vz = *reinterpret_cast<const uint4*>(st + S::V_ZEROS + 16 * (8 * i + g));
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const float2 z = float2_of(word(vz, 2 * e + r)), sv = float2_of(word(vs[i], 2 * e + r));
+                const float za = fmaf((float)kMid, sv.x, z.x), zb = fmaf((float)kMid, sv.y, z.y);
+#pragma unroll
+                for (int k = 0; k < HT; ++k) {
+                  zs[2 * r][k] = fmaf(p[i][e][k], za, zs[2 * r][k]);
+                  zs[2 * r + 1][k] = fmaf(p[i][e][k], zb, zs[2 * r + 1][k]);
+                }
+              }
+          }
+        }
+        // ================================================================ value sums
+        constexpr int NR = S::PAIR ? 2 : 4;  // rounds: a pair of groups or one group each
+#pragma unroll
+        for (int rd = 0; rd < NR; ++rd) {
+          uint32_t b[4][NP][2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (S::PAIR) {
+                b[i][0][e] = transpose8(hmul2(ph[i][e][0], word(vs[i], 2 * e + rd)));
+              } else if (!PREC) {
+                const uint32_t sv = dup_half(word(vs[i], 2 * e + (rd >> 1)), rd & 1);
+#pragma unroll
+                for (int t = 0; t < NH; ++t) b[i][t][e] = transpose8(hmul2(ph[i][e][t], sv));
+              } else {
+                const float2 s2 = float2_of(word(vs[i], 2 * e + (rd >> 1)));
+                const float sv = (rd & 1) ? s2.y : s2.x;
+                if (HC == 4) {
+                  const float v = p[i][e][0] * sv;
+                  const float hi = __half2float(__float2half_rn(v));
+                  b[i][0][e] = transpose8(half2_of(hi, (v - hi) * 2048.0f));
+                } else {
+#pragma unroll
+                  for (int t = 0; t < NH; ++t) {
+                    const float v0 = p[i][e][(2 * t) % HT] * sv, v1 = p[i][e][(2 * t + 1) % HT] * sv;
+                    const uint32_t hi = half2_of(v0, v1);
+                    const float2 f = float2_of(hi);
+                    b[i][t][e] = transpose8(hi);
+                    b[i][(NP / 2 + t) % NP][e] = transpose8(half2_of((v0 - f.x) * 2048.0f, (v1 - f.y) * 2048.0f));
+                  }
                 }
               }
             }
-          }
-        // minus the codes' middle times the sum of the rounded P' (all rows alike)
-        float base[NP][4];
-        if (MODE == kF16) {
-          constexpr uint32_t c0 = VB == 4 ? 0x80088008u : 0x80028002u, c1 = VB == 4 ? 0x80808080u : 0x80088008u;
-#pragma unroll
-          for (int np = 0; np < NP; ++np) {
-            mma16z(base[np], c0, c1, c0, c1, b[0][np][0], b[0][np][1]);
-#pragma unroll
-            for (int i = 1; i < 4; ++i) mma16(base[np], c0, c1, c0, c1, b[i][np][0], b[i][np][1]);
-          }
-        }
-        constexpr int MT = S::PAIR ? 4 : 2;  // 16-channel tiles of this round
-#pragma unroll
-        for (int mm = 0; mm < MT; ++mm) {
-          const int m = rd * MT + mm;
-          const uint4 w = *reinterpret_cast<const uint4*>(st + ((VB == 4 ? m : m >> 1) * 8 + g) * 64 + cq * 16);
-          const uint32_t m0 = VB == 4 ? 0x000F000Fu : (m & 1) ? 0x00300030u : 0x00030003u;
-          const uint32_t m1 = VB == 4 ? 0x00F000F0u : (m & 1) ? 0x00C000C0u : 0x000C000Cu;
-          float d[NP][4];
+          // minus the codes' middle times the sum of the rounded P' (all rows alike)
+          float base[NP][4];
           if (MODE == kF16) {
-#pragma unroll
-            for (int np = 0; np < NP; ++np)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) d[np][r] = (VB == 2 && (m & 1)) ? 16.0f * base[np][r] : base[np][r];
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t x = word(w, i), xs = x >> 8;
-            constexpr int f1 = VB == 4 ? 16 : 4;  // the fields' factors
-            const int f = VB == 4 ? 1 : (m & 1) ? 16 : 1;
-            const uint32_t a0 = codes_of<PREC>(x, m0, f * kMid), a1 = codes_of<PREC>(x, m1, f * f1 * kMid);
-            const uint32_t a2 = codes_of<PREC>(xs, m0, f * kMid), a3 = codes_of<PREC>(xs, m1, f * f1 * kMid);
+            constexpr uint32_t c0 = VB == 4 ? 0x80088008u : 0x80028002u, c1 = VB == 4 ? 0x80808080u : 0x80088008u;
 #pragma unroll
             for (int np = 0; np < NP; ++np) {
-              if (i == 0 && MODE != kF16)
-                mma16z(d[np], a0, a1, a2, a3, b[i][np][0], b[i][np][1]);
-              else
-                mma16(d[np], a0, a1, a2, a3, b[i][np][0], b[i][np][1]);
+              mma16z(base[np], c0, c1, c0, c1, b[0][np][0], b[0][np][1]);
+#pragma unroll
+              for (int i = 1; i < 4; ++i) mma16(base[np], c0, c1, c0, c1, b[i][np][0], b[i][np][1]);
             }
           }
-          if (S::PAIR) {  // columns of this tile's group of the pair
-            const int odd = (m >> 1) & 1;
-            O[m][0] += d[0][odd];
-            O[m][1] += d[0][2 + odd];
-          } else if (HC == 4) {
-            O[m][0] += fmaf(d[0][1], kLow, d[0][0]);
-            O[m][1] += fmaf(d[0][3], kLow, d[0][2]);
-          } else {
+          constexpr int MT = S::PAIR ? 4 : 2;  // 16-channel tiles of this round
 #pragma unroll
-            for (int t = 0; t < NH; ++t)
+          for (int mm = 0; mm < MT; ++mm) {
+            const int m = rd * MT + mm;
+            const uint4 w = *reinterpret_cast<const uint4*>(st + ((VB == 4 ? m : m >> 1) * 8 + g) * 64 + cq * 16);
+            const uint32_t m0 = VB == 4 ? 0x000F000Fu : (m & 1) ? 0x00300030u : 0x00030003u;
+            const uint32_t m1 = VB == 4 ? 0x00F000F0u : (m & 1) ? 0x00C000C0u : 0x000C000Cu;
+            float d[NP][4];
+            if (MODE == kF16) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                O[m][4 * t + r] += PREC ? fmaf(d[(NP / 2 + t) % NP][r], kLow, d[t][r]) : d[t][r];
+              for (int np = 0; np < NP; ++np)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) d[np][r] = (VB == 2 && (m & 1)) ? 16.0f * base[np][r] : base[np][r];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t x = word(w, i), xs = x >> 8;
+              constexpr int f1 = VB == 4 ? 16 : 4;  // the fields' factors
+              const int f = VB == 4 ? 1 : (m & 1) ? 16 : 1;
+              const uint32_t a0 = codes_of<PREC>(x, m0, f * kMid), a1 = codes_of<PREC>(x, m1, f * f1 * kMid);
+              const uint32_t a2 = codes_of<PREC>(xs, m0, f * kMid), a3 = codes_of<PREC>(xs, m1, f * f1 * kMid);
+#pragma unroll
+              for (int np = 0; np < NP; ++np) {
+                if (i == 0 && MODE != kF16)
+                  mma16z(d[np], a0, a1, a2, a3, b[i][np][0], b[i][np][1]);
+                else
+                  mma16(d[np], a0, a1, a2, a3, b[i][np][0], b[i][np][1]);
+              }
+            }
+            if (S::PAIR) {  // columns of this tile's group of the pair
+              const int odd = (m >> 1) & 1;
+              O[m][0] += d[0][odd];
+              O[m][1] += d[0][2 + odd];
+            } else if (HC == 4) {
+              O[m][0] += fmaf(d[0][1], kLow, d[0][0]);
+              O[m][1] += fmaf(d[0][3], kLow, d[0][2]);
+            } else {
+#pragma unroll
+              for (int t = 0; t < NH; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  O[m][4 * t + r] += PREC ? fmaf(d[(NP / 2 + t) % NP][r], kLow, d[t][r]) : d[t][r];
+            }
           }
         }
       }
-    }
-    __syncwarp();  // every lane has read the slot
-    if (j + SV < n) issue_values(j + SV, sv);
-    if (++sv == SV) {
-      sv = 0;
-      pv ^= 1;
-    }
-    if (j + 1 == n || tiles[(j + 1) & 63].unit != unit) end_segment();
+      __syncwarp();  // every lane has read the slot
+      if (j + SV < n) issue_values(j + SV, sv);
+      if (++sv == SV) {
+        sv = 0;
+        pv ^= 1;
+      }
+      ++j;
+    } while (j < n && tiles[j & 63].unit == unit);
+    if (!landed) break;
+    end_segment();
+    if (j == n) break;
+    unit = tiles[j & 63].unit;
+    load_query(unit, raw0);
   }
-  if (__builtin_expect(j < n, 0)) {
+  if (__builtin_expect(!landed, 0)) {
     // a copy did not land in time: not-a-number partials for this segment and the
     // rest of the range, and time for copies in flight to land before the
     // shared memory is given up
@@ -1018,8 +1036,8 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
     }
     __nanosleep(64000);
   }
+  if (lane == 0) a.status[rank] = landed ? 0 : 1;
   let_next_start();
-  if (lane == 0) a.status[rank] = j < n;
 }
 
 template <int KB, int VB, int HC, int MODE, bool CH0>
