@@ -4,6 +4,8 @@
 * ``lib/libkvq_checked.so`` -- the same with -DKVQ_BOUNDS_CHECK: every checked
   cache, partial and window access compares its range with the array's extent,
   skips and counts an access out of bounds (``kvq_bounds_violations``).
+* ``lib/kvq_torch.so`` -- the Python binding of the paged cache's calls (C++, torch's
+  headers), which checks tensors and calls the library.
 * ``lib/libkvqgen.so`` -- the seeded input generator (plain C + OpenMP).
 
 The quantizer inside libkvq relies on IEEE-rounded fp32 subtract/divide and
@@ -74,8 +76,30 @@ def build_kvq(force: bool = False, verbose_ptxas: bool = False, checked: bool = 
     return so
 
 
+def build_binding(force: bool = False) -> str:
+    os.makedirs(LIB_DIR, exist_ok=True)
+    src = os.path.join(CSRC, "torch_binding.cpp")
+    so = os.path.join(LIB_DIR, "kvq_torch.so")
+    if force or _newer(so, [src, os.path.join(INCLUDE, "kvq.h")]):
+        import sysconfig
+
+        import torch
+
+        root = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(NVCC))
+        inc = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+        lib = os.path.join(root, "lib")
+        subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+                               *[f"-I{d}" for d in inc], src, "-o", so, f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda",
+                               "-ltorch_cpu", "-ltorch_python"])
+    return so
+
+
 def build_all(force: bool = False) -> None:
     build_gen(force)
+    build_binding(force)
     build_kvq(force)
     build_kvq(force, checked=True)
 

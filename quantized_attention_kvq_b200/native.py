@@ -1,4 +1,6 @@
-"""Thin ctypes binding of ``lib/libkvq.so`` (C ABI in ``include/kvq.h``).
+"""Thin binding of ``lib/libkvq.so`` (C ABI in ``include/kvq.h``): ctypes, and for the paged
+cache's calls, several of which make up a serving step of a few microseconds each, the compiled
+argument checks of ``lib/kvq_torch.so``.
 
 Argument marshalling only: every step of the path runs in the library's CUDA
 kernels.  torch supplies device memory and the current CUDA stream.  There is
@@ -7,6 +9,7 @@ no CPU fallback; a missing library or a non-CUDA tensor raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 
@@ -389,14 +392,24 @@ def _call(dev: int, stream, what: str, fn, *args):
         raise KvqError(status, what)
 
 
-def _rows(t: torch.Tensor, name: str, heads: int) -> tuple[int, int]:
-    """(pointer, row stride in elements) of [rows][heads][128] with contiguous heads."""
-    if t.dim() != 3 or t.shape[1:] != (heads, 128):
-        raise ValueError(f"{name} is [rows][{heads}][128]")
-    n, (a, b, c) = t.shape[0], t.stride()
-    if n and (c != 1 or (heads > 1 and b != 128)):
-        raise ValueError(f"{name}: a row's heads and channels are contiguous")
-    return t.data_ptr(), a if n > 1 else heads * 128
+_fast = None
+
+
+def _binding():
+    """The compiled argument checks of the paged cache's calls (lib/kvq_torch.so), bound to this library."""
+    global _fast
+    if _fast is None:
+        path = os.path.join(os.path.dirname(LIB_PATH), "kvq_torch.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location("kvq_torch", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        L = lib()
+        m.bind(*(ctypes.cast(f, _P).value for f in (L.kvq_page_plan, L.kvq_paged_append, L.kvq_paged_gather,
+                                                    L.kvq_paged_decode, L.kvq_paged_decode_workspace_bytes)), KvqError)
+        _fast = m
+    return _fast
 
 
 class PagePlan:
@@ -414,6 +427,7 @@ class PagePlanner:
 
     def __init__(self, num_pages: int, page_tokens: int = 64):
         self.num_pages, self.page_tokens = num_pages, page_tokens
+        self._plan = _binding().plan
 
     def plan(self, ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
              free_pages: torch.Tensor, free_count: torch.Tensor, n_slots: int, done: torch.Tensor | None = None,
@@ -422,30 +436,11 @@ class PagePlanner:
         [num_pages], both updated in place; free_count: int32 [1].  Returns the new tokens' slots and
         positions [n_slots], cu_new [B + 1], the sequence lengths [B] and the free pages left [1]; `out`
         reuses an earlier plan's tensors (its seq_lens may be ctx_lens, its free_count free_count)."""
-        if block_table.dim() != 2:
-            raise ValueError("block_table is [B][max_pages]")
-        B, max_pages = block_table.shape
-        dev = _device_of(ctx_lens, new_lens, block_table, free_pages, free_count, done)
-        if out is None:  # one allocation, its tensors one after another
-            head = (2 * B + 5) & ~3  # cu_new, seq_lens and free_count, then 16-byte aligned slots and positions
-            tail = (n_slots + 3) & ~3
-            buf = ctx_lens.new_empty(head + 2 * tail)
-            c, s, f, _, n, _, p, _ = buf.split_with_sizes((B + 1, B, 1, head - 2 * B - 2, n_slots, tail - n_slots, n_slots,
-                                                           tail - n_slots))
-            out = PagePlan(n, p, c, s, f)
-            cu = buf.data_ptr()
-            lens, left, slots = cu + 4 * (B + 1), cu + 4 * (2 * B + 1), cu + 4 * head
-            pos = slots + 4 * tail
-        else:
-            _device_of(ctx_lens, out.slots, out.positions, out.cu_new, out.seq_lens, out.free_count)
-            slots, pos = _i32(out.slots, "slots", n_slots), _i32(out.positions, "positions", n_slots)
-            cu, lens = _i32(out.cu_new, "cu_new", B + 1), _i32(out.seq_lens, "seq_lens", B)
-            left = _i32(out.free_count, "free_count", 1)
-        _call(dev, stream, "kvq_page_plan", lib().kvq_page_plan, self.num_pages, self.page_tokens, B,
-              _i32(ctx_lens, "ctx_lens", B), _i32(new_lens, "new_lens", B), _i32(done, "done", B),
-              _i32(block_table, "block_table", B, max_pages), max_pages,
-              _i32(free_pages, "free_pages", self.num_pages), _i32(free_count, "free_count", 1), left, slots, pos, n_slots,
-              cu, lens)
+        if out is None:
+            return PagePlan(*self._plan(self.num_pages, self.page_tokens, ctx_lens, new_lens, block_table, free_pages,
+                                        free_count, n_slots, done, None, stream and stream.cuda_stream))
+        self._plan(self.num_pages, self.page_tokens, ctx_lens, new_lens, block_table, free_pages, free_count, n_slots, done,
+                   (out.slots, out.positions, out.cu_new, out.seq_lens, out.free_count), stream and stream.cuda_stream)
         return out
 
 
@@ -471,37 +466,19 @@ class PagedKVQCache:
         self.desc.pages = _dev_ptr(pages)
         self.num_pages, self.H, self.page_tokens = num_pages, H, page_tokens
         self.planner = PagePlanner(num_pages, page_tokens)
-        L = lib()
-        self._decode, self._append, self._gather = L.kvq_paged_decode, L.kvq_paged_append, L.kvq_paged_gather
+        self._at, self._dev = ctypes.addressof(self.desc), pages.get_device()
+        fast = _binding()
+        self._decode, self._append, self._gather = fast.decode, fast.append, fast.gather
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor, stream=None):
         """k_new, v_new: [n][H][128] (fp32 / bf16 / fp16), rows at any 16-byte stride; slots: int32 [n]."""
-        dev = _device_of(k_new, v_new, slots, self.pages)
-        if k_new.dtype != v_new.dtype or k_new.shape != v_new.shape:
-            raise ValueError("k_new and v_new have one type and shape")
-        k, ks = _rows(k_new, "k_new", self.H)
-        v, vs = _rows(v_new, "v_new", self.H)
-        n = k_new.shape[0]
-        _call(dev, stream, "kvq_paged_append", self._append, self._ref, k, ks, v, vs,
-              torch_dtype_code(k_new.dtype), n, _i32(slots, "slots", n))
+        self._append(self._at, self.H, self._dev, k_new, v_new, slots, stream and stream.cuda_stream)
 
     def gather(self, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16, rotate_back: bool = True,
                k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, stream=None):
         """The cached tokens' keys and values as dense rows [n][H][128] of `dtype`."""
-        n = slots.shape[0]
-        shape = (n, self.H, 128)
-        dev = _device_of(slots, k_out, v_out, self.pages)
-        if k_out is None:
-            k_out = slots.new_empty(shape, dtype=dtype)
-        elif k_out.shape != shape or k_out.dtype is not dtype or not k_out.is_contiguous():
-            raise ValueError(f"k_out is a contiguous {list(shape)} of {dtype}")
-        if v_out is None:
-            v_out = slots.new_empty(shape, dtype=dtype)
-        elif v_out.shape != shape or v_out.dtype is not dtype or not v_out.is_contiguous():
-            raise ValueError(f"v_out is a contiguous {list(shape)} of {dtype}")
-        _call(dev, stream, "kvq_paged_gather", self._gather, self._ref, _i32(slots, "slots", n), n,
-              torch_dtype_code(dtype), int(rotate_back), k_out.data_ptr(), v_out.data_ptr())
-        return k_out, v_out
+        return self._gather(self._at, self.H, self._dev, slots, torch_dtype_code(dtype), rotate_back, k_out, v_out,
+                            stream and stream.cuda_stream)
 
     def select(self, q: torch.Tensor, keep_groups: int, mask_out: torch.Tensor | None = None, stream=None):
         """q: [B][Hq][128] contiguous; the kept channel groups [B][H] (int32 bits) for decode's mask
@@ -525,24 +502,9 @@ class PagedKVQCache:
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """q: [B][Hq][128], rows at any 16-byte stride; block_table: int32 [B][max_pages]; seq_lens: int32 [B];
         returns [B][Hq][128] of q's type."""
-        B, Hq, _ = q.shape
-        qp, qs = _rows(q, "q", Hq)
-        dev = _device_of(q, block_table, seq_lens, mask, out, workspace, self.pages)
-        if out is None:
-            out = q.new_empty((B, Hq, 128))
-        elif out.shape != (B, Hq, 128) or out.dtype is not q.dtype or not out.is_contiguous():
-            raise ValueError(f"out is a contiguous [{B}][{Hq}][128] of {q.dtype}")
-        if workspace is None:
-            workspace = q.new_empty(max(self.workspace_bytes(B, Hq), 256), dtype=torch.uint8)
-        elif not workspace.is_contiguous():
-            raise ValueError("workspace is contiguous")
-        max_pages = block_table.shape[-1]
-        _call(dev, stream, "kvq_paged_decode", self._decode, self._ref, qp, qs, _DTYPE_CODES[q.dtype], Hq, B,
-              _i32(block_table, "block_table", B, max_pages), max_pages, _i32(seq_lens, "seq_lens", B), max_len,
-              None if mask is None else _i32(mask, "mask", B, self.H),
-              0.08838834764831845 if softmax_scale is None else softmax_scale, out.data_ptr(), workspace.data_ptr(),
-              workspace.nbytes)
-        return out
+        return self._decode(self._at, self.H, self._dev, q, block_table, seq_lens, max_len, mask,
+                            0.08838834764831845 if softmax_scale is None else softmax_scale, out, workspace,
+                            stream and stream.cuda_stream)
 
     def decode_status(self, batch: int, q_heads: int, workspace: torch.Tensor, stream=None) -> int:
         """Status of the last decode that used `workspace`: KVQ_OK or KVQ_ERR_TIMEOUT (synchronizes the stream)."""

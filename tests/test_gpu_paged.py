@@ -569,3 +569,22 @@ def test_wrapper_refusals_on_the_device():
         c.append(q[:, :2], q[:, :2].float(), i32([0, 1]))
     with pytest.raises(ValueError):
         c.append(q[:, :2], q[:, 2:], i32([0, 1, 2]))
+    with pytest.raises(ValueError):
+        c.append(q[:, :2, :64], q[:, :2, :64], i32([0, 1]))
+    with pytest.raises(ValueError):
+        c.append(q[:, :2].transpose(0, 1), q[:, :2].transpose(0, 1), i32([0, 1]))
+    with pytest.raises(ValueError):
+        c.append(q[:, :2].double(), q[:, :2].double(), i32([0, 1]))
+    with pytest.raises(ValueError):
+        c.gather(i32([0, 1]), torch.float16, k_out=q[:, :2].contiguous())
+    with pytest.raises(ValueError):
+        c.gather(i32([0, 1]).long())
+    with pytest.raises(ValueError):
+        c.decode(q, table, lens, 1 << 40)
+    with pytest.raises(TypeError):
+        c.decode(q, table, lens, 1.5)
+    with pytest.raises(TypeError):
+        c.decode(q, table, lens, 128, softmax_scale="x")
+    before = c.pages.clone()
+    c.append(q[:, :2], q[:, 2:], i32([0, 1]))  # heads out of a wider row: fine
+    assert not torch.equal(before, c.pages)

@@ -149,15 +149,19 @@ def test_wrapper_refuses_host_tensors_and_wrong_shapes(L):
         native.PagedKVQCache(4, 2, 4, 4, pages=torch.zeros(16, dtype=torch.uint8))
     cache = native.PagedKVQCache.__new__(native.PagedKVQCache)  # no device memory is needed to refuse
     cache.desc, cache.H, cache.pages = desc(), 2, torch.zeros(8, dtype=torch.uint8)
-    cache._ref = ctypes.byref(cache.desc)
-    k = torch.zeros(3, 2, 128)
-    with pytest.raises(ValueError):
-        cache.append(k, k, torch.zeros(3, dtype=torch.int32))
-    with pytest.raises(ValueError):
-        native._rows(torch.zeros(3, 2, 64), "k", 2)
-    with pytest.raises(ValueError):
-        native._rows(torch.zeros(2, 3, 128).transpose(0, 1), "k", 2)
-    assert native._rows(torch.zeros(3, 10, 128)[:, 2:4], "k", 2)[1] == 1280
+    cache._at, cache._dev = ctypes.addressof(cache.desc), -1
+    fast = native._binding()
+    cache._append, cache._gather, cache._decode = fast.append, fast.gather, fast.decode
+    k, i = torch.zeros(3, 2, 128), torch.zeros(3, dtype=torch.int32)
+    for bad in (lambda: cache.append(k, k, i), lambda: cache.gather(i), lambda: cache.append(k, None, i),
+                lambda: cache.append(k, k, [1, 2, 3]), lambda: cache.decode(k, i[None], i, 3),
+                lambda: native.PagePlanner(4).plan(i, i, i[:, None], i, i[:1], 3),
+                lambda: native.PagePlanner(4).plan(i, i, i, i, i[:1], 3)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: fast.append(1, 2), lambda: cache.gather(i, rotate_back="x"), lambda: fast.bind("x", 1, 1, 1, 1, 1)):
+        with pytest.raises((TypeError, ValueError)):
+            bad()
     with pytest.raises(ValueError):
         native._i32(torch.zeros(3), "slots", 3)
     with pytest.raises(ValueError):
