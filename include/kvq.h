@@ -227,7 +227,9 @@ KVQ_API kvq_status kvq_decode_status(const kvq_cache* cache, int32_t q_heads, co
  * calling host thread leaves tile `tile` of its first CTA unfilled (its ring
  * stage never completes), so the waits on that tile give up after about a
  * second and kvq_decode_status reports KVQ_ERR_TIMEOUT.  A negative tile
- * clears the hook.  Not for production use.
+ * clears the hook.  The next paged decode takes it too: tile `tile` of its
+ * first warp's range, reported by kvq_paged_decode_status.  Not for production
+ * use.
  */
 KVQ_API void kvq_test_withhold_tile(int32_t tile);
 
@@ -428,9 +430,9 @@ KVQ_API size_t kvq_paged_bytes(const kvq_paged_cache* cache);
  *     (ctx + new <= max_pages * page_tokens), its new tokens fit the slot
  *     array (cu_new[b + 1] <= n_slots), and it needs no page or the pages
  *     needed by the requests up to and including it (those that fit) do not
- *     exceed the free pages.  Pages are popped from the top of the stack in request order and written to
- *     block_table[b][ceil(ctx / page_tokens) ...]; other entries stay as they
- *     were.
+ *     exceed the free pages.  Pages are popped from the top of the stack in
+ *     request order and written to block_table[b][ceil(ctx / page_tokens) ...];
+ *     other entries stay as they were.
  *  3. The new tokens of all requests form one list, request after request:
  *     cu_new[b] is request b's first index in it (cu_new[batch] the total,
  *     saturated at 2^31 - 1).  slots[n] and positions[n] of list entry n are
@@ -444,7 +446,8 @@ KVQ_API size_t kvq_paged_bytes(const kvq_paged_cache* cache);
  * free_count, free_count_out: device int32, may be the same word; slots: device
  * int32 [n_slots]; positions: device int32 [n_slots] or NULL; cu_new: device
  * int32 [batch + 1]; seq_lens_out: device int32 [batch], may be ctx_lens.
- * No other arrays may overlap.  batch up to 8192 (more: KVQ_ERR_UNSUPPORTED).
+ * No other arrays may overlap.  batch up to 8192, n_slots up to 2^30 (more:
+ * KVQ_ERR_UNSUPPORTED).
  */
 KVQ_API kvq_status kvq_page_plan(int32_t num_pages, int32_t page_tokens, int32_t batch, const int32_t* ctx_lens,
                                  const int32_t* new_lens, const int32_t* done, int32_t* block_table,
@@ -464,7 +467,7 @@ KVQ_API kvq_status kvq_page_plan(int32_t num_pages, int32_t page_tokens, int32_t
  *  starts 16-byte aligned.
  *  slots: device int32 [n]; a slot outside the pool (-1: padding) skips its
  *  token.  The slots inside the pool must be distinct.  No other token's bytes
- *  change.  n == 0 is a no-op.
+ *  change.  n == 0 is a no-op; n > 2^30: KVQ_ERR_UNSUPPORTED.
  */
 KVQ_API kvq_status kvq_paged_append(const kvq_paged_cache* cache, const void* k_new, int64_t k_stride,
                                     const void* v_new, int64_t v_stride, kvq_dtype dtype, int32_t n,
@@ -477,7 +480,7 @@ KVQ_API kvq_status kvq_paged_append(const kvq_paged_cache* cache, const void* k_
  * fp32 butterflies), rounded once to `dtype`.
  *  k_out, v_out: device [n][kv_heads][128] of `dtype`, 16-byte aligned; either
  *  may be NULL (not read back).  slots as in kvq_paged_append, repetitions
- *  allowed; rows of slots outside the pool are zero.  n == 0 is a no-op.
+ *  allowed; rows of slots outside the pool are zero.  n as there.
  */
 KVQ_API kvq_status kvq_paged_gather(const kvq_paged_cache* cache, const int32_t* slots, int32_t n, kvq_dtype dtype,
                                     int32_t rotate_back, void* k_out, void* v_out, void* stream);

@@ -156,14 +156,6 @@ DecodePlan plan_decode(const kvq_cache* c, int32_t q_heads) {
   return p;
 }
 
-// test hook: the tile the next split decode of this host thread withholds
-thread_local int g_withheld_tile = -1;
-int take_withheld_tile() {
-  const int t = g_withheld_tile;
-  g_withheld_tile = -1;
-  return t;
-}
-
 // which halves of the decode to enqueue
 enum { kRunSplit = 1, kRunCombine = 2 };
 

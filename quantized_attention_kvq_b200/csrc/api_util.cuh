@@ -8,6 +8,15 @@
 #include "common.cuh"
 
 namespace kvq {
+
+// test hook: the tile the next split decode of this host thread withholds
+inline thread_local int g_withheld_tile = -1;
+inline int take_withheld_tile() {
+  const int t = g_withheld_tile;
+  g_withheld_tile = -1;
+  return t;
+}
+
 namespace {
 
 // One NVTX range per enqueueing ABI call (named after it), so that a

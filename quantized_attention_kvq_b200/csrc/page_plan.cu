@@ -40,7 +40,10 @@ __device__ __forceinline__ int find(const int* sum, int n, int x) {
   return lo;
 }
 
-__device__ __forceinline__ int pages_for(int tokens, int P) { return tokens / P + (tokens % P != 0); }
+__device__ __forceinline__ int pages_for(int tokens, const Divisor& P) {
+  const int q = P.quotient(tokens);
+  return q + ((uint32_t)q * P.d != (uint32_t)tokens);
+}
 
 __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PlanArgs a) {
   extern __shared__ int sm[];
@@ -70,12 +73,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PlanArgs a) {
         const bool fin = a.done && a.done[b] != 0;
         const int c = max(a.ctx[b], 0);
         t0 += max(a.add[b], 0);
-        t1 += fin ? min(pages_for(c, P), a.max_pages) : 0;
+        t1 += fin ? min(pages_for(c, a.page), a.max_pages) : 0;
         ctx[b] = fin ? 0 : c;
       } else {
         const long long end = (long long)ctx[b] + max(a.add[b], 0);
         const bool fits = end <= row_tokens && cu[b + 1] <= a.n_slots;
-        t0 += fits ? pages_for((int)end, P) - pages_for(ctx[b], P) : 0;
+        t0 += fits ? pages_for((int)end, a.page) - pages_for(ctx[b], a.page) : 0;
       }
     }
     long long x0 = t0, x1 = t1;
@@ -118,13 +121,13 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PlanArgs a) {
       if (pass == 0) {
         const bool fin = a.done && a.done[b] != 0;
         s[0] += max(a.add[b], 0);
-        s[1] += fin ? min(pages_for(max(a.ctx[b], 0), P), a.max_pages) : 0;
+        s[1] += fin ? min(pages_for(max(a.ctx[b], 0), a.page), a.max_pages) : 0;
         cu[b + 1] = (int)min(s[0], kMax);
         give[b + 1] = (int)min(s[1], kMax);
       } else {
         const long long end = (long long)ctx[b] + max(a.add[b], 0);
         const bool fits = end <= row_tokens && cu[b + 1] <= a.n_slots;
-        s[0] += fits ? pages_for((int)end, P) - pages_for(ctx[b], P) : 0;
+        s[0] += fits ? pages_for((int)end, a.page) - pages_for(ctx[b], a.page) : 0;
         need[b + 1] = (int)min(s[0], kMax);
       }
     }
@@ -141,9 +144,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PlanArgs a) {
   if ((tid & 31) == 0) atomicMax(&taken_s, mine);
 
   const int gt = blockIdx.x * kPlanThreads + tid, gn = gridDim.x * kPlanThreads;
-  for (int r = gt; r < returned; r += gn) {
+  for (int r = gt; r < top - count; r += gn) {  // all of them, unless lengths were wrong and the stack is full
     const int b = find(give, B, r);
-    if (count + r < a.num_pages) a.free_pages[count + r] = a.table[(size_t)b * a.max_pages + (r - give[b])];
+    a.free_pages[count + r] = a.table[(size_t)b * a.max_pages + (r - give[b])];
   }
   if (gridDim.x > 1)
     cg::this_cluster().sync();  // pushed pages visible; every CTA has read what is updated in place
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PlanArgs a) {
 
   for (int j = gt; j < taken; j += gn) {
     const int b = find(need, B, j);
-    a.table[(size_t)b * a.max_pages + pages_for(ctx[b], P) + (j - need[b])] = a.free_pages[top - 1 - j];
+    a.table[(size_t)b * a.max_pages + pages_for(ctx[b], a.page) + (j - need[b])] = a.free_pages[top - 1 - j];
   }
   // a thread takes four consecutive list entries: one search, then steps to the
   // next request; entries on one page share its look-up
@@ -172,14 +175,14 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PlanArgs a) {
       int pg = -1;  // the page to look up
       if (b != first) {
         first = b;
-        held = pages_for(ctx[b], P);
+        held = pages_for(ctx[b], a.page);
         const bool fits = (long long)ctx[b] + (cu[b + 1] - cu[b]) <= row_tokens && cu[b + 1] <= a.n_slots;
         served = fits && (need[b + 1] == need[b] || need[b + 1] <= top);
         p = ctx[b] + (n - cu[b]);
-        pg = p / P;
+        pg = a.page.quotient(p);
         off = p - pg * P;
       } else if (off == P) {
-        pg = p / P;
+        pg = a.page.quotient(p);
         off = 0;
       }
       if (!served) continue;

@@ -10,6 +10,7 @@ constexpr int kBlockTokens = 64;    // tokens of one block (one kv head's part o
 constexpr int kScaleBytes = 512;    // one fp16 per token and 32-channel group
 constexpr int kMaxPageTokens = 4096;
 constexpr int kMaxPlanBatch = 8192;
+constexpr int kMaxRows = 1 << 30;  // of one slot list: indexes stay below 2^31
 
 // Byte offsets of a block's parts.  The key codes come first and everything
 // else follows in one piece, so that a decode that keeps all channel groups
@@ -82,7 +83,20 @@ cudaError_t launch_overlapped(void (*kern)(Args...), dim3 grid, dim3 block, size
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// x / d for 0 <= x < 2^31 and 2 <= d < 2^31 by a multiplication: with 2^(l-1) < d <= 2^l,
+// m = floor(2^(31+l) / d) + 1 exceeds 2^(31+l) / d by at most 1, which x < 2^31 cannot tell
+struct Divisor {
+  uint32_t d, m;
+  int shift;
+  explicit Divisor(int by = 2) : d((uint32_t)by), shift(0) {
+    while ((1ull << (shift + 1)) < d) ++shift;
+    m = (uint32_t)((1ull << (32 + shift)) / d + 1);
+  }
+  __device__ __forceinline__ int quotient(int x) const { return (int)(__umulhi((uint32_t)x, m) >> shift); }
+};
+
 struct PlanArgs {
+  Divisor page;  // by page_tokens
   int num_pages, page_tokens, batch, max_pages, n_slots;
   const int32_t *ctx, *add, *done;
   int32_t *table, *free_pages;
@@ -122,6 +136,7 @@ struct PagedDecodeArgs {
   float2* part_ml;   // [units + ranks][G] (running max, running sum)
   int32_t* starts;   // [B + 1] first tile of each request, times H
   int32_t* status;   // [kPagedMaxRanks] 1 where a bounded wait of the rank gave up
+  int withheld_tile; // test hook: rank 0 never fills this tile's ring slot (-1: none)
   size_t part_rows;
 };
 // The tiles of a decode are spread over ranks: the warps of one CTA per SM.  More

@@ -104,10 +104,11 @@ KVQ_API kvq_status kvq_page_plan(int32_t num_pages, int32_t page_tokens, int32_t
                        free_count_out, slots, positions, cu_new,      seq_lens_out};
   for (const void* p : all)
     if (!aligned4(p)) return KVQ_ERR_INVALID_ARG;
-  if (batch > kMaxPlanBatch || page_tokens % kBlockTokens != 0 || page_tokens > kMaxPageTokens ||
+  if (batch > kMaxPlanBatch || n_slots > kMaxRows || page_tokens % kBlockTokens != 0 || page_tokens > kMaxPageTokens ||
       (int64_t)num_pages * page_tokens > INT32_MAX || (int64_t)max_pages * page_tokens > INT32_MAX)
     return KVQ_ERR_UNSUPPORTED;
   PlanArgs a;
+  a.page = Divisor(page_tokens);
   a.num_pages = num_pages;
   a.page_tokens = page_tokens;
   a.batch = batch;
@@ -138,6 +139,7 @@ KVQ_API kvq_status kvq_paged_append(const kvq_paged_cache* c, const void* k_new,
   if (!slots || !aligned4(slots) || !rows_ok(k_new, k_stride, c->kv_heads, dtype) ||
       !rows_ok(v_new, v_stride, c->kv_heads, dtype))
     return KVQ_ERR_INVALID_ARG;
+  if (n > kMaxRows) return KVQ_ERR_UNSUPPORTED;
   PagedAppendArgs a;
   a.c = paged_view(c);
   a.k = k_new;
@@ -160,6 +162,7 @@ KVQ_API kvq_status kvq_paged_gather(const kvq_paged_cache* c, const int32_t* slo
   if (n == 0) return KVQ_OK;
   if (!slots || !aligned4(slots) || (!k_out && !v_out) || !aligned16(k_out) || !aligned16(v_out))
     return KVQ_ERR_INVALID_ARG;
+  if (n > kMaxRows) return KVQ_ERR_UNSUPPORTED;
   PagedGatherArgs a;
   a.c = paged_view(c);
   a.slots = slots;
@@ -216,6 +219,7 @@ KVQ_API kvq_status kvq_paged_decode(const kvq_paged_cache* c, const void* q, int
   a.starts = reinterpret_cast<int32_t*>(ws + p.starts_offset);
   a.status = reinterpret_cast<int32_t*>(ws + p.status_offset);
   a.part_rows = p.rows;
+  a.withheld_tile = take_withheld_tile();
   return cuda_status(launch_paged_decode(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(256) k_paged_join(PagedDecodeArgs a, int max_r
 #pragma unroll
     for (int k = 1; k < 8; ++k) {
       const float2 o = sml[k];
-      const float w = o.x == -INFINITY ? 0.0f : exp2f(o.x - mn);
+      const float w = o.x == -INFINITY && o.y == 0.0f ? 0.0f : exp2f(o.x - mn);  // not-a-number sums stay in
       const float4 v = sacc[k][lane];
       s.l = fmaf(w, o.y, s.l);
       s.acc[0] = fmaf(w, v.x, s.acc[0]);

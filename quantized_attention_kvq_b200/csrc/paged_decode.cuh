@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
   };
   auto issue_values = [&](int j, int s) {
     if (lane == 0) {
+      if (j == a.withheld_tile && rank == 0) return;
       const int block = tiles[j & 63].block;
       mbar_arrive_expect_tx(vbars + 8 * s, block >= 0 ? S::VPART : 0);
       if (block >= 0)

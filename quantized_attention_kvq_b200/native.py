@@ -399,7 +399,7 @@ def _binding():
     """The compiled argument checks of the paged cache's calls (lib/kvq_torch.so), bound to this library."""
     global _fast
     if _fast is None:
-        path = os.path.join(os.path.dirname(LIB_PATH), "kvq_torch.so")
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "kvq_torch.so")
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build()")
         spec = importlib.util.spec_from_file_location("kvq_torch", path)

@@ -166,6 +166,33 @@ def test_appended_tokens_hold_the_oracles_bits(kb, vb, rot, ch0, rotv, clip, dty
     assert np.array_equal(got, want)  # the tokens' bytes are the oracle's, every other byte is as it was
 
 
+@pytest.mark.parametrize("kb,vb", [(4, 4), (4, 2), (2, 4), (2, 2)])
+@pytest.mark.parametrize("start,P", [(0, 64), (1, 64), (3, 128), (6, 64), (61, 192)])
+def test_tokens_in_a_row_hold_the_same_bytes_as_one_by_one(kb, vb, start, P):
+    # a request's consecutive tokens from any place in their page, over page ends, with a
+    # hole and a second request: the order in which a call lists them does not show
+    H, num, n = 2, 12, 257
+    table = np.array([7, 2, 3, 11, 0, 9])
+    pos = start + np.arange(n)
+    slots = table[pos // P] * P + pos % P
+    slots[100] = -1
+    slots[200:] = np.setdiff1d(np.arange(num * P), slots)[5:5 + n - 200]
+    k, v = rows(9 + start, n, H, "bf16")
+    perm = np.random.RandomState(start).permutation(n)
+    pools = []
+    for order in (np.arange(n), perm):
+        cache = native.PagedKVQCache(num, H, kb, vb, page_tokens=P, keep_ch0=1)
+        cache.pages.fill_(0x5A)
+        o = torch.from_numpy(order).cuda()
+        cache.append(k[o].contiguous(), v[o].contiguous(), i32(slots[order]))
+        pools.append(cache.pages)
+    one = native.PagedKVQCache(num, H, kb, vb, page_tokens=P, keep_ch0=1)
+    one.pages.fill_(0x5A)
+    for j in range(n):
+        one.append(k[j:j + 1], v[j:j + 1], i32(slots[j:j + 1]))
+    assert torch.equal(pools[0], one.pages) and torch.equal(pools[1], one.pages)
+
+
 def test_append_one_token_and_none():
     cache = native.PagedKVQCache(2, 1, 4, 4)
     before = cache.pages.clone()

@@ -88,6 +88,7 @@ def test_append_refusals(L):
     assert call(ks=255) == INVALID and call(vs=-256) == INVALID  # less than a row
     assert call(ks=260) == INVALID                               # rows off 16-byte boundaries
     assert call(n=0, k=None, v=None, slots=None) == native.KVQ_OK
+    assert call(n=(1 << 30) + 1) == UNSUPPORTED
 
 
 def test_gather_refusals(L):
@@ -99,6 +100,7 @@ def test_gather_refusals(L):
     assert call(slots=None) == INVALID and call(k=None, v=None) == INVALID
     assert call(k=FAKE + 4) == INVALID and call(v=FAKE + 8) == INVALID
     assert call(n=0, k=None, v=None, slots=None) == native.KVQ_OK
+    assert call(n=(1 << 30) + 1) == UNSUPPORTED
 
 
 def test_decode_refusals(L):
