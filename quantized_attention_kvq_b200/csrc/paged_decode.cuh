@@ -18,7 +18,9 @@
 //           the fp16 subnormal c * 2^-24 (times 4, 16 or 64 at the higher bit
 //           fields, taken out again by the query): unpacking costs one AND per
 //           two codes and a shift per eight, no conversion.  The query enters as
-//           two fp16 pieces, q = hi + lo * 2^-11, in columns of their own.  One
+//           two fp16 pieces, for up to four heads in columns of their own (low pieces
+//           times 2^11), for more in products of their own that continue the same
+//           sums: half the accumulators.  One
 //           accumulator per quantization group, so the per-token scale applies
 //           exactly afterwards; the zero-point sums are one more product of the
 //           fp16 zeros with the per-group query sums.
@@ -71,6 +73,8 @@ template <int KB, int VB, int HC, int MODE, bool CH0>
 struct Shape {
   static constexpr bool PREC = MODE == kF32;
   static constexpr int NT = HC / 4;               // 8-column tiles of the query operand (two pieces per head)
+  static constexpr int NA = HC == 4 ? 1 : HC / 8;  // 8-column tiles of scores
+  static constexpr float LOW = HC == 4 ? 1.0f / 2048.0f : 1.0f;  // weight of a low piece of the query
   static constexpr int HT = HC / 4;               // heads per thread
   static constexpr int NH = HC == 4 ? 1 : HC / 8;  // 8-column tiles of heads
   static constexpr int NP = NH * (PREC && HC > 4 ? 2 : 1);  // 8-column tiles of P'
@@ -138,6 +142,11 @@ __device__ __forceinline__ void mma8z(float (&d)[4], uint32_t a0, uint32_t a1, u
   asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
+}
+__device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0));
 }
 // 8x8 transpose of 16-bit elements held two per lane
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
@@ -227,7 +236,7 @@ template <int KB, int VB, int HC, int MODE, bool CH0>
 __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_paged_decode(PagedDecodeArgs a) {
   using S = Shape<KB, VB, HC, MODE, CH0>;
   constexpr bool PREC = S::PREC;
-  constexpr int W = S::WARPS, TH = S::THREADS, NT = S::NT, HT = S::HT, NH = S::NH, NP = S::NP, OC = S::OC;
+  constexpr int W = S::WARPS, TH = S::THREADS, NT = S::NT, NA = S::NA, HT = S::HT, NH = S::NH, NP = S::NP, OC = S::OC;
   extern __shared__ __align__(128) uint8_t smem[];
   const PagedView& c = a.c;
   // the warp's number through a shuffle: the compiler then knows it to be the same
@@ -450,6 +459,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
   float smax = 0.0f, plim = kTop16;  // largest value scale met, bound of p that keeps P' in fp16
 
   constexpr int kTop = PREC ? 6 : 14;
+  constexpr float kUp = 1.0f / S::LOW;
   constexpr float kCode = PREC ? 1.0f : 1.0f / 16777216.0f;  // what a code of 1 is to the matrix unit
 
   // ---- a segment's query: rotated, masked, split into pieces, as fragments.
@@ -536,10 +546,10 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
           }
           const uint32_t h01 = half2_of(y[0], y[1]), h23 = half2_of(y[2], y[3]);
           const float2 f01 = float2_of(h01), f23 = float2_of(h23);
-          e[0] = (y[0] - f01.x) * 2048.0f;
-          e[1] = (y[1] - f01.y) * 2048.0f;
-          e[2] = (y[2] - f23.x) * 2048.0f;
-          e[3] = (y[3] - f23.y) * 2048.0f;
+          e[0] = (y[0] - f01.x) * kUp;
+          e[1] = (y[1] - f01.y) * kUp;
+          e[2] = (y[2] - f23.x) * kUp;
+          e[3] = (y[3] - f23.y) * kUp;
           const uint32_t l01 = half2_of(e[0], e[1]), l23 = half2_of(e[2], e[3]);
           if (KB == 4) {  // step part, column i
             if (live) {
@@ -568,7 +578,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
           const __half hi = __float2half_rn(y);
           __half* z = reinterpret_cast<__half*>(qz);
           z[(nt_hi * 32 + n_hi * 4 + (Q >> 1)) * 2 + (Q & 1)] = hi;
-          z[(nt_lo * 32 + n_lo * 4 + (Q >> 1)) * 2 + (Q & 1)] = __float2half_rn((y - __half2float(hi)) * 2048.0f);
+          z[(nt_lo * 32 + n_lo * 4 + (Q >> 1)) * 2 + (Q & 1)] = __float2half_rn((y - __half2float(hi)) * kUp);
         }
         if (part == 0) {
           const float f = a.scale_log2 * __int_as_float((127 + (PREC ? 0 : 24) - ex) << 23);
@@ -659,17 +669,18 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
       if (nval > 0) {
         const uint8_t* st = kring + sk * S::KPART;
         // ================================================================ scores
-        float acc[4][NT][4];
+        float acc[4][NA][4];
         {
           const uint4 z0 = *reinterpret_cast<const uint4*>(st + S::K_ZEROS + (g * 2 + (cq & 1)) * 16);
           const uint4 z1 = *reinterpret_cast<const uint4*>(st + S::K_ZEROS + ((8 + g) * 2 + (cq & 1)) * 16);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t bz = qz[nt * 32 + lane];
+          for (int na = 0; na < NA; ++na) {
+            const uint32_t bz = qz[na * 32 + lane], bl = HC == 4 ? 0 : qz[((NT - NA) + na) * 32 + lane];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint4& z = i < 2 ? z0 : z1;
-              mma8z(acc[i][nt], (i & 1) ? z.z : z.x, (i & 1) ? z.w : z.y, bz);
+              mma8z(acc[i][na], (i & 1) ? z.z : z.x, (i & 1) ? z.w : z.y, bz);
+              if (HC > 4) mma8(acc[i][na], (i & 1) ? z.z : z.x, (i & 1) ? z.w : z.y, bl);
             }
           }
         }
@@ -727,14 +738,18 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
             const float2 sa = float2_of((Q >> 1) ? ks[i].y : ks[i].x), sb = float2_of((Q >> 1) ? ks[i].w : ks[i].z);
             const float s0 = (Q & 1) ? sa.y : sa.x, s1 = (Q & 1) ? sb.y : sb.x;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int na = 0; na < NA; ++na) {
               float d[4];
-              mma16z(d, ka[0], ka[1], ka[2], ka[3], bA[nt].x, bA[nt].y);
-              mma16(d, ka[4], ka[5], ka[6], ka[7], bB[nt].x, bB[nt].y);
-              acc[i][nt][0] = fmaf(s0, d[0], acc[i][nt][0]);
-              acc[i][nt][1] = fmaf(s0, d[1], acc[i][nt][1]);
-              acc[i][nt][2] = fmaf(s1, d[2], acc[i][nt][2]);
-              acc[i][nt][3] = fmaf(s1, d[3], acc[i][nt][3]);
+              mma16z(d, ka[0], ka[1], ka[2], ka[3], bA[NT - NA + na].x, bA[NT - NA + na].y);
+              mma16(d, ka[4], ka[5], ka[6], ka[7], bB[NT - NA + na].x, bB[NT - NA + na].y);
+              if (HC > 4) {  // the low pieces came first
+                mma16(d, ka[0], ka[1], ka[2], ka[3], bA[na].x, bA[na].y);
+                mma16(d, ka[4], ka[5], ka[6], ka[7], bB[na].x, bB[na].y);
+              }
+              acc[i][na][0] = fmaf(s0, d[0], acc[i][na][0]);
+              acc[i][na][1] = fmaf(s0, d[1], acc[i][na][1]);
+              acc[i][na][2] = fmaf(s1, d[2], acc[i][na][2]);
+              acc[i][na][3] = fmaf(s1, d[3], acc[i][na][3]);
             }
           }
         }
@@ -753,9 +768,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
             const float kv = __uint_as_float(e ? kk & 0xFFFF0000u : kk << 16);
 #pragma unroll
             for (int k = 0; k < HT; ++k) {
-              const float hi = HC == 4 ? acc[i][0][2 * e] : acc[i][k >> 1][2 * e + (k & 1)];
-              const float lo = HC == 4 ? acc[i][0][2 * e + 1] : acc[i][NT / 2 + (k >> 1)][2 * e + (k & 1)];
-              float sc = fmaf(lo, kLow, hi);
+              float sc = HC == 4 ? fmaf(acc[i][0][2 * e + 1], kLow, acc[i][0][2 * e]) : acc[i][k >> 1][2 * e + (k & 1)];
               if (CH0) sc = fmaf(q0[k], kv, sc);
               p[i][e][k] = sc;
             }

@@ -12,6 +12,7 @@ namespace kvq {
 namespace {
 
 constexpr int kGatherWarps = 4;
+constexpr int kGatherBlocks = 10;  // per SM: 48 registers a thread (no bound: 56 and 9 blocks, 2 us more for 32K tokens of 8 heads)
 
 // Orthonormal Walsh-Hadamard transform of a row held by four lanes as above, in
 // fp32: x[8k + r] is channel 32k + 8g + r, so the stages 1, 2, 4, 32 and 64 stay in
@@ -63,7 +64,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half*) {
 }
 
 template <int KB, int VB, typename Out>
-__global__ void __launch_bounds__(kGatherWarps * 32) k_paged_gather(PagedGatherArgs a) {
+__global__ void __launch_bounds__(kGatherWarps * 32, kGatherBlocks) k_paged_gather(PagedGatherArgs a) {
   const PagedView& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane & 3;
