@@ -501,7 +501,10 @@ KVQ_API size_t kvq_paged_decode_workspace_bytes(const kvq_paged_cache* cache, in
  *        max_pages * page_tokens (larger: KVQ_ERR_CAPACITY).  A request with no
  *        token gets a zero row.
  *  mask: device uint32 [batch][kv_heads] kept channel groups, as
- *        kvq_select_channels writes it, or NULL = all; only kept rows are read.
+ *        kvq_select_channels writes it, or NULL = all.  Key rows of groups that
+ *        are not kept contribute nothing; INT4 keys with up to four query heads
+ *        a kv head and 16-bit types do not read them either (elsewhere picking
+ *        rows costs more time than their bytes).
  *  out:  device [batch][q_heads][128] of `dtype`.  For 16-bit types the
  *        probabilities are rounded to fp16 before the value sums; for fp32 they
  *        keep 22 bits.

@@ -78,6 +78,12 @@ struct Shape {
   static constexpr int HT = HC / 4;               // heads per thread
   static constexpr int NH = HC == 4 ? 1 : HC / 8;  // 8-column tiles of heads
   static constexpr int NP = NH * (PREC && HC > 4 ? 2 : 1);  // 8-column tiles of P'
+  // with a mask, whether only kept key rows are copied: it saves bytes and costs some
+  // 100 instructions a tile, so only where bytes are what a decode waits for.
+  // INT4 keys and values, 4 heads a group, 32K tokens x 8: 54, 56 and 61 us with 8,
+  // 20 and 28 of 32 groups kept against 64 for whole blocks; INT2 at 128K x 4: 94
+  // against 88 whatever is kept; INT4 / INT2 with 8 heads a group: 134 against 127.
+  static constexpr bool PIECES = KB == 4 && HC == 4 && !PREC;
   static constexpr bool PAIR = HC == 4 && !PREC;  // P' columns: (head, group of a pair)
   static constexpr int OC = HC == 4 ? 2 : HC / 2;  // fp32 sums per thread and 16-channel tile
   static constexpr int WARPS = paged_decode_warps(HC, PREC);
@@ -276,9 +282,9 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
   for (int i = lane; i < (S::QF + S::QZ + S::QH) / 16; i += 32)  // columns of absent heads stay zero
     reinterpret_cast<uint4*>(mine)[i] = make_uint4(0, 0, 0, 0);
   if (lane == 0) {
-    // with a mask every lane copies key rows and arrives beside the bulk copy of the rest
+    // PIECES: every lane copies key rows and arrives beside the bulk copy of the rest
     for (int s = 0; s < kMaxSlots; ++s) {
-      mbar_init(kbars + 8 * s, a.mask ? 33 : 1);
+      mbar_init(kbars + 8 * s, S::PIECES && a.mask ? 33 : 1);
       mbar_init(vbars + 8 * s, 1);
     }
     mbar_fence_init();
@@ -369,11 +375,11 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
   };
   look_up(0);
 
-  // ---- ring copies.  Without a mask a block's key part is one bulk copy.  With
-  // one, its kept rows are spread over the lanes in 16-byte pieces (a bulk copy
-  // per run of rows costs some 15 instructions each, issued one lane at a
-  // time); lane's q-th piece is piece 32 q + lane of the kept rows, and where
-  // the pieces are changes with the unit only.
+  // ---- ring copies.  A block's key part is one bulk copy.  PIECES with a mask: its
+  // kept rows are spread over the lanes in 16-byte pieces (a bulk copy per run of
+  // rows costs some 15 instructions each, issued one lane at a time); lane's
+  // q-th piece is piece 32 q + lane of the kept rows, and where the pieces are
+  // changes with the unit only.
   constexpr int KROW = kBlockTokens * KB / 2;  // bytes of a key row of 4 channels
   constexpr int PPR = KROW / 16, NPC = PPR;  // pieces per row, and per lane
   uint32_t run_msk = kFull;
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
     const Tile d = tiles[j & 63];
     const uint32_t bar = kbars + 8 * s, dst = smem_addr(kring + s * S::KPART);
     const uint8_t* src = c.pages + (size_t)d.block * c.block_bytes;
-    if (!a.mask) {
+    if (!S::PIECES || !a.mask) {
       if (lane == 0) {
         mbar_arrive_expect_tx(bar, d.block >= 0 ? S::KPART : 0);
         if (d.block >= 0) bulk_g2s(dst, src, S::KPART, bar);
