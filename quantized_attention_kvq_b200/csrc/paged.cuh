@@ -140,7 +140,9 @@ struct PagedDecodeArgs {
   size_t part_rows;
 };
 // The tiles of a decode are spread over ranks: the warps of one CTA per SM.  More
-// warps hide more latency, as long as their registers do not spill.
+// warps hide more latency, as long as their registers and rings fit: 8 heads a group
+// take 134 us with 12 warps and 146 with 14, a number the four schedulers cannot share
+// evenly (ragged batch of 64, INT4 / INT2).
 constexpr int kPagedSms = 148;
 constexpr int paged_decode_warps(int padded_heads, bool f32) {
   return f32 || padded_heads == 16 ? 8 : padded_heads == 8 ? 12 : 16;

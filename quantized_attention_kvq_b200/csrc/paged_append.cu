@@ -7,7 +7,11 @@
 // grid: twice the parallelism in a decode step's small append, and half the
 // registers.
 //
-// Bound by instruction issue.  A rotated row is loaded with its channels
+// Bound by instruction issue (54% of the slots, fp64 and its conversions a fifth of
+// that each) and by latencies at 20 warps a SM: 84 us for 32K tokens of 8 heads
+// (INT4 keys, INT2 values; 164 MB of input).  Tried and slower: writing words of
+// eight neighbouring tokens instead of bytes (92 us), persistent blocks that fetch
+// their next rows ahead (108 us).  A rotated row is loaded with its channels
 // interleaved over the four lanes, so that five of the seven stages stay in the
 // lane; one pass through shared memory (16-byte pieces, swizzled so that both
 // sides are free of bank conflicts) then brings lane g its own group, and the
@@ -24,7 +28,7 @@ namespace kvq {
 namespace {
 
 constexpr int kAppendWarps = 4;
-constexpr int kAppendBlocks = 5;  // per SM: 96 registers a thread; 6 or 7 spill (121, 131, 152 us at 32K tokens of 8 heads with the read-back)
+constexpr int kAppendBlocks = 5;  // per SM: 96 registers a thread; 6 or 7 spill (121, 131, 152 us with the read-back)
 
 // eight consecutive input elements, widened
 __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {

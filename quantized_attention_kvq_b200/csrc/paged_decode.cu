@@ -86,7 +86,9 @@ __device__ __forceinline__ void finish_row(const PagedDecodeArgs& a, size_t row,
 }
 
 // WPR warps per output row: one where a row has few partials (a block then takes
-// eight rows), eight where its sequence was cut into many.  A row's partials sit
+// eight rows), eight where its sequence was cut into many: 16 ranks a unit or more
+// (us of the whole decode with one and eight: 296 units of 8 ranks 39 and 44; 128 of 18
+// 22.2 and 22.0; 64 of 37 67.8 and 62.8; 8 of 296 64 and 24).  A row's partials sit
 // in slots unit + r of the ranks r its tiles touch, as the split cut them.
 template <int WPR>
 __global__ void __launch_bounds__(256) k_paged_join(PagedDecodeArgs a, int max_ranks) {
@@ -145,7 +147,7 @@ cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t s) {
                                   : (a.c.v_bits == 4 ? launch_24(a, s) : launch_22(a, s));
   if (e != cudaSuccess) return e;
   const int ranks = paged_decode_ranks(a.G, a.dtype), rows = a.B * a.Hq;
-  if (ranks / ((long long)a.B * a.c.H) >= 8) return launch_overlapped(k_paged_join<8>, dim3(rows), dim3(256), 0, s, a, ranks);
+  if (ranks / ((long long)a.B * a.c.H) >= 16) return launch_overlapped(k_paged_join<8>, dim3(rows), dim3(256), 0, s, a, ranks);
   return launch_overlapped(k_paged_join<1>, dim3((rows + 7) / 8), dim3(256), 0, s, a, ranks);
 }
 
