@@ -544,46 +544,46 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
       const int nt_hi = HC == 16 ? j >> 3 : 0, nt_lo = HC == 4 ? 0 : HC == 8 ? 1 : 2 + (j >> 3);
       const int n_hi = HC == 4 ? 2 * j : j & 7, n_lo = HC == 4 ? 2 * j + 1 : j & 7;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float y[4], e[4];
-          if (KB == 4) {  // (channels 0, 2), (1, 3) / 16, minus what a whole byte brings of the upper field
-            y[0] = x[4 * i];
-            y[1] = x[4 * i + 2];
-            y[2] = x[4 * i + 1] * (1.0f / 16.0f) - (PREC ? 0.0f : y[0]);
-            y[3] = x[4 * i + 3] * (1.0f / 16.0f) - (PREC ? 0.0f : y[1]);
-          } else {
-            y[0] = x[4 * i];
-            y[1] = x[4 * i + 1] * 0.25f;
-            y[2] = x[4 * i + 2] * 0.0625f;
-            y[3] = x[4 * i + 3] * 0.015625f;
+      for (int i = 0; i < 4; ++i) {
+        float y[4], e[4];
+        if (KB == 4) {  // (channels 0, 2), (1, 3) / 16, minus what a whole byte brings of the upper field
+          y[0] = x[4 * i];
+          y[1] = x[4 * i + 2];
+          y[2] = x[4 * i + 1] * (1.0f / 16.0f) - (PREC ? 0.0f : y[0]);
+          y[3] = x[4 * i + 3] * (1.0f / 16.0f) - (PREC ? 0.0f : y[1]);
+        } else {
+          y[0] = x[4 * i];
+          y[1] = x[4 * i + 1] * 0.25f;
+          y[2] = x[4 * i + 2] * 0.0625f;
+          y[3] = x[4 * i + 3] * 0.015625f;
+        }
+        const uint32_t h01 = half2_of(y[0], y[1]), h23 = half2_of(y[2], y[3]);
+        const float2 f01 = float2_of(h01), f23 = float2_of(h23);
+        e[0] = (y[0] - f01.x) * kUp;
+        e[1] = (y[1] - f01.y) * kUp;
+        e[2] = (y[2] - f23.x) * kUp;
+        e[3] = (y[3] - f23.y) * kUp;
+        const uint32_t l01 = half2_of(e[0], e[1]), l23 = half2_of(e[2], e[3]);
+        if (KB == 4) {  // step part, column i
+          if (live) {
+            reinterpret_cast<uint2*>(qf)[(part * NT + nt_hi) * 32 + n_hi * 4 + i] = make_uint2(h01, h23);
+            reinterpret_cast<uint2*>(qf)[(part * NT + nt_lo) * 32 + n_lo * 4 + i] = make_uint2(l01, l23);
           }
-          const uint32_t h01 = half2_of(y[0], y[1]), h23 = half2_of(y[2], y[3]);
-          const float2 f01 = float2_of(h01), f23 = float2_of(h23);
-          e[0] = (y[0] - f01.x) * kUp;
-          e[1] = (y[1] - f01.y) * kUp;
-          e[2] = (y[2] - f23.x) * kUp;
-          e[3] = (y[3] - f23.y) * kUp;
-          const uint32_t l01 = half2_of(e[0], e[1]), l23 = half2_of(e[2], e[3]);
-          if (KB == 4) {  // step part, column i
-            if (live) {
-              reinterpret_cast<uint2*>(qf)[(part * NT + nt_hi) * 32 + n_hi * 4 + i] = make_uint2(h01, h23);
-              reinterpret_cast<uint2*>(qf)[(part * NT + nt_lo) * 32 + n_lo * 4 + i] = make_uint2(l01, l23);
-            }
-          } else {
-            // steps 2 Q (channels 0, 1) and 2 Q + 1 (channels 2, 3), column i; a word's
-            // low half is of the even lane's group, its high half of the odd lane's:
-            // the even lane writes the high pieces of both, the odd one the low pieces
-            const bool odd = part & 1;
-            const uint32_t own01 = odd ? l01 : h01, own23 = odd ? l23 : h23;
-            const uint32_t got01 = __shfl_xor_sync(kFull, odd ? h01 : l01, 1), got23 = __shfl_xor_sync(kFull, odd ? h23 : l23, 1);
-            const uint32_t e01 = odd ? got01 : own01, o01 = odd ? own01 : got01, e23 = odd ? got23 : own23, o23 = odd ? own23 : got23;
-            if (live) {
-              uint2* q2 = reinterpret_cast<uint2*>(qf) + ((part & ~1) * NT + (odd ? nt_lo : nt_hi)) * 32 + (odd ? n_lo : n_hi) * 4 + i;
-              q2[0] = make_uint2(__byte_perm(e01, o01, 0x5410), __byte_perm(e01, o01, 0x7632));
-              q2[NT * 32] = make_uint2(__byte_perm(e23, o23, 0x5410), __byte_perm(e23, o23, 0x7632));
-            }
+        } else {
+          // steps 2 Q (channels 0, 1) and 2 Q + 1 (channels 2, 3), column i; a word's
+          // low half is of the even lane's group, its high half of the odd lane's:
+          // the even lane writes the high pieces of both, the odd one the low pieces
+          const bool odd = part & 1;
+          const uint32_t own01 = odd ? l01 : h01, own23 = odd ? l23 : h23;
+          const uint32_t got01 = __shfl_xor_sync(kFull, odd ? h01 : l01, 1), got23 = __shfl_xor_sync(kFull, odd ? h23 : l23, 1);
+          const uint32_t e01 = odd ? got01 : own01, o01 = odd ? own01 : got01, e23 = odd ? got23 : own23, o23 = odd ? own23 : got23;
+          if (live) {
+            uint2* q2 = reinterpret_cast<uint2*>(qf) + ((part & ~1) * NT + (odd ? nt_lo : nt_hi)) * 32 + (odd ? n_lo : n_hi) * 4 + i;
+            q2[0] = make_uint2(__byte_perm(e01, o01, 0x5410), __byte_perm(e01, o01, 0x7632));
+            q2[NT * 32] = make_uint2(__byte_perm(e23, o23, 0x5410), __byte_perm(e23, o23, 0x7632));
           }
         }
+      }
       if (live) {
         if ((part & 1) == 0) {  // group part / 2: K positions 2 c + b of the zero-point product
           const int Q = part >> 1;

@@ -42,7 +42,7 @@ def check_plan(got, want):
 @pytest.mark.parametrize("seed,B,P,max_pages,short,n_cut", [
     (1, 1, 64, 1, 0, 0), (2, 1, 64, 3, 0, 0), (3, 7, 64, 20, 0, 0), (4, 7, 128, 5, 9, 0), (5, 64, 64, 40, 30, 0),
     (6, 511, 64, 12, 100, 0), (7, 513, 256, 6, 0, 700), (8, 3000, 64, 9, 500, 0), (9, 8192, 64, 4, 0, 3000),
-    (10, 40, 64, 90, 0, 0), (11, 33, 4096, 2, 3, 0)])
+    (10, 40, 64, 90, 0, 0), (11, 33, 4096, 2, 3, 0), (12, 700, 64, 3, 40, 10**6)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_plan_matches_requests_taken_one_by_one(seed, B, P, max_pages, short, n_cut, in_place):
     r = np.random.RandomState(seed)

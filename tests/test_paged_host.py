@@ -19,6 +19,7 @@ INVALID, UNSUPPORTED, CAPACITY, WORKSPACE = (native.KVQ_ERR_INVALID_ARG, native.
 def L():
     from quantized_attention_kvq_b200 import build
     build.build_kvq()
+    build.build_binding()
     return native.lib()
 
 
