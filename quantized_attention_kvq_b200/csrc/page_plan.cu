@@ -272,7 +272,7 @@ static int plan_ctas() {
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&clusters, k_page_plan<1024>, &cfg) == cudaSuccess && clusters > 0) n = kWidest;
   }
-  cudaGetLastError();
+  if (n == kPortable) cudaGetLastError();  // a refused question is not the caller's error
   known[dev].store(n, std::memory_order_relaxed);
   return n;
 }

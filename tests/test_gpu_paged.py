@@ -573,6 +573,85 @@ def test_two_streams_and_a_repeated_call_give_the_same_bits():
         assert pool.cache.decode_status(B, Hq, w) == native.KVQ_OK
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_work_joined_from_another_stream(captured):
+    # the kernels may be placed early, but see what other streams' work before them left,
+    # and leave what later work there must not touch
+    H, G, T, P = 2, 4, 640, 64
+    cache = native.PagedKVQCache(T // P, H, 4, 4)
+    first, then = (rows(3 + i, T, H, "bf16") for i in range(2))
+    slots, table = i32(np.arange(T)), i32([list(range(T // P))])
+    q = torch.randn(1, H * G, D, device="cuda", dtype=torch.bfloat16)
+    lens, ws = i32([T]), torch.empty(cache.workspace_bytes(1, H * G), dtype=torch.uint8, device="cuda")
+    cache.append(*first, slots)
+    want = cache.decode(q, table, lens, T, workspace=ws).clone()
+    cache.append(*then, slots)
+    other = cache.decode(q, table, lens, T, workspace=ws).clone()
+    assert not torch.equal(want, other)
+    out, out2, k, v = torch.empty_like(want), torch.empty_like(want), torch.empty(T, H, D, device="cuda"), torch.empty(T, H, D, device="cuda")
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def work():
+        side.wait_stream(main)
+        cache.gather(slots, torch.float32, k_out=k, v_out=v)  # a kernel that lets the next one start early
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1000000)
+            cache.append(*first, slots)
+        out.zero_()
+        main.wait_stream(side)
+        cache.decode(q, table, lens, T, workspace=ws, out=out)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            cache.append(*then, slots)
+            cache.gather(slots, torch.float32, k_out=k, v_out=v)
+        main.wait_stream(side)
+        cache.decode(q, table, lens, T, workspace=ws, out=out2)
+
+    torch.cuda.synchronize()
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=main):
+            work()
+    for _ in range(3):
+        out.zero_()
+        out2.zero_()
+        torch.cuda.synchronize()
+        if captured:
+            g.replay()
+        else:
+            with torch.cuda.stream(main):
+                work()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(out2, other)
+
+
+def test_tokens_that_are_no_numbers_stay_by_themselves():
+    # infinities and not-a-numbers in some tokens of one head: no other token's bytes, no other
+    # head's outputs change, and requests that do not hold them keep their outputs
+    H, G, T, P = 2, 2, 256, 64
+    k, v = rows(11, T, H, "bf16")
+    bad = [(5, float("inf")), (6, float("nan")), (70, float("-inf"))]
+    clean = native.PagedKVQCache(4, H, 4, 2, keep_ch0=1)
+    dirty = native.PagedKVQCache(4, H, 4, 2, keep_ch0=1)
+    slots = i32(np.arange(T))
+    clean.append(k, v, slots)
+    k2, v2 = k.clone(), v.clone()
+    for t, x in bad:
+        k2[t, 0, 9] = x
+        v2[t, 0, 77] = x
+    dirty.append(k2, v2, slots)
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[[t for t, _ in bad]] = False
+    for a, b in zip(clean.gather(slots, torch.float32), dirty.gather(slots, torch.float32)):
+        assert torch.equal(a[keep], b[keep]) and torch.equal(a[:, 1], b[:, 1])
+    q = torch.randn(4, H * G, D, device="cuda", dtype=torch.bfloat16)
+    table, lens = i32([[0, 1], [2, 3], [1, -1], [0, -1]]), i32([128, 100, 6, 5])
+    a, b = clean.decode(q, table, lens, 128), dirty.decode(q, table, lens, 128)
+    assert torch.equal(a[:, G:], b[:, G:])   # the other head
+    assert torch.equal(a[1:], b[1:])         # requests that hold no such token, or end before it
+
+
 def test_wrapper_refusals_on_the_device():
     pool = Pool(13, 6, 2, 64, 4, 4, 0)
     c = pool.cache
