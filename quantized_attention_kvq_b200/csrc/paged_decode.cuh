@@ -48,7 +48,9 @@
 // 2^-8 of a bf16 output.  P' rounded to fp16 errs by 2^-11 of p * scale * code;
 // codes counted from their middle (code - 8, code - 2) halve what that
 // multiplies, which an fp16 output can tell: there the middle times the
-// sum of the rounded P' is subtracted by one more product per group.  For fp32
+// sum of the rounded P' is subtracted by one more product per group, and the middle
+// times the sum of p * scale is added in fp32 (in fp16 that product passes the type's
+// range for rotated values whose outputs do not).  For fp32
 // outputs the codes become normal fp16 numbers (a mask with an OR of 1024 and
 // one subtraction), P' comes from the fp32 p and keeps a second fp16 piece, the
 // zero-point sums are fp32 FMAs, and the value codes are counted from their
@@ -111,6 +113,7 @@ struct Shape {
   static constexpr int K_CH0 = BlockLayout(KB, VB, CH0).k0, KPART = BlockLayout(KB, VB, CH0).vc;
   static constexpr int V_SCALES = kBlockTokens * kHeadDim * VB / 8, V_ZEROS = V_SCALES + kScaleBytes;
   static constexpr int VPART = V_ZEROS + kScaleBytes;
+  static constexpr int MID = VB == 4 ? 8 : 2;  // the middle of the value codes
   // ring slots per warp: as many as fit, keys first
   static constexpr int slots(bool keys) {
     int k = 1, v = 1;
@@ -637,8 +640,12 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
       }
       if (!PREC) {  // group r: row r (even tokens) and row 12 + r (odd ones) of the zeros' product
 #pragma unroll
-        for (int r = 0; r < kGroups; ++r)
-          zs[r][k] = __shfl_sync(kFull, zp[k >> 1][k & 1], 4 * r + cq) + __shfl_sync(kFull, zp[k >> 1][2 + (k & 1)], 16 + 4 * r + cq);
+        for (int r = 0; r < kGroups; ++r) {
+          const float lo = zp[k >> 1][k & 1], hi = zp[k >> 1][2 + (k & 1)];
+          zs[r][k] = __shfl_sync(kFull, lo, 4 * r + cq) + __shfl_sync(kFull, hi, 16 + 4 * r + cq);
+          if (MODE == kF16)  // and the codes' middle times the scales' sums
+            zs[r][k] = fmaf(S::MID, __shfl_sync(kFull, hi, 4 * r + cq) + __shfl_sync(kFull, lo, 16 + 4 * r + cq), zs[r][k]);
+        }
       }
     }
     constexpr float kOne = 1.0f / kCode;
@@ -891,7 +898,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
               p[i][e][k] = x[i][e][k];
               l[k] += x[i][e][k];
             }
-        constexpr int kMid = VB == 4 ? 8 : 2;
+        constexpr int kMid = S::MID;
         uint32_t ph[4][2][NH];  // p as fp16: the head twice (HC = 4), or a pair of heads
         if (!PREC) {
 #pragma unroll
@@ -904,24 +911,23 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
           // zero-point sums: matrix i's transposed rows are (e, group), its columns the
           // tokens 8u + 2i + e; rows 0-3 meet the even tokens in the lower half of K,
           // rows 12-15 the odd ones in the upper half, the others are not used
-          uint4 z = load_transposed(smem_addr(st + S::V_ZEROS + 16 * lane));
-          if (MODE == kF16) {  // codes are counted from their middle: z + middle * scale
-            const uint4 zs4 = load_transposed(smem_addr(st + S::V_SCALES + 16 * lane));
-            const __half2 mid = __float2half2_rn((float)kMid);
-            uint32_t* zw = &z.x;
-            const uint32_t* sw = &zs4.x;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __half2 r = __hfma2(mid, *reinterpret_cast<const __half2*>(&sw[i]), *reinterpret_cast<const __half2*>(&zw[i]));
-              zw[i] = *reinterpret_cast<const uint32_t*>(&r);
-            }
-          }
+          const uint4 z = load_transposed(smem_addr(st + S::V_ZEROS + 16 * lane));
+          // kF16 counts codes from their middle, and the middle times the scale may pass fp16
+          // where value and output do not (rotated values): the scales' sums are rows of their
+          // own, in the places that are free: 4-7 the odd tokens', 8-11 the even ones'
+          const uint4 vt = MODE == kF16 ? load_transposed(smem_addr(st + S::V_SCALES + 16 * lane)) : make_uint4(0, 0, 0, 0);
+          auto add_zeros = [&](float (&d)[4], int i, uint32_t b0, uint32_t b1) {
+            const uint32_t zi = word(z, i), si = word(vt, i);
+            if (MODE == kF16)
+              mma16(d, g < 4 ? zi : 0u, g < 4 ? si : 0u, g < 4 ? 0u : si, g < 4 ? 0u : zi, b0, b1);
+            else
+              mma16(d, zi, 0u, 0u, zi, b0, b1);
+          };
 #pragma unroll
           for (int t = 0; t < NH; ++t) {
-            float d[4];
-            mma16z(d, z.x, 0u, 0u, z.x, transpose8(ph[0][0][t]), transpose8(ph[0][1][t]));
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int i = 1; i < 4; ++i) mma16(d, word(z, i), 0u, 0u, word(z, i), transpose8(ph[i][0][t]), transpose8(ph[i][1][t]));
+            for (int i = 0; i < 4; ++i) add_zeros(d, i, transpose8(ph[i][0][t]), transpose8(ph[i][1][t]));
 #pragma unroll
             for (int r = 0; r < 4; ++r) zp[t][r] += d[r];
           }

@@ -1,0 +1,58 @@
+"""The paged cache on the GPU at the ends of its ranges, against values in 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from paged_testlib import BT, D, Layout, attention, hadamard, output_bound
+from quantized_attention_kvq_b200 import native
+from test_gpu_paged import TYPES, Pool, decode_case, i32
+
+pytestmark = pytest.mark.gpu
+
+
+def held(cache, lay, h):
+    """Keys and values [num_pages * page_tokens][128] of head h in 64 bits, as the pool's bytes hold them."""
+    raw = cache.pages.cpu().numpy().reshape(cache.num_pages, cache.H, cache.page_tokens // BT, lay.bytes)
+    kv = [lay.values(b) for b in raw[:, h].reshape(-1, lay.bytes)]
+    return np.concatenate([x[0] for x in kv]), np.concatenate([x[1] for x in kv])
+
+
+# ------------------------------------------------------------- large rotated values
+@pytest.mark.parametrize("kb,vb,value", [(4, 4, 12000.0), (4, 4, -12000.0), (2, 2, 12000.0), (4, 2, 24000.0), (2, 4, 32000.0)])
+@pytest.mark.parametrize("dtype,G", [("f16", 1), ("f16", 5), ("f16", 16), ("bf16", 4), ("f32", 4)])
+def test_decode_of_large_equal_values_taken_back_through_the_rotation(kb, vb, value, dtype, G):
+    # A row of equal values is one large channel after the rotation, sqrt(128) times the value: beyond
+    # fp16, though its scale, its zero and the output fit.
+    n, P = 130, 64
+    cache = native.PagedKVQCache(3, 1, kb, vb, page_tokens=P, rotate_v=1)
+    g = torch.Generator(device="cuda").manual_seed(kb + vb)
+    k = torch.randn(n, 1, D, device="cuda", generator=g).half()
+    cache.append(k, torch.full((n, 1, D), value, device="cuda", dtype=torch.float16), i32(np.arange(n)))
+    q = torch.randn(1, G, D, device="cuda", generator=g).to(TYPES[dtype])
+    out = cache.decode(q, i32([[0, 1, 2]]), i32([n]), n)
+    kh, vh = (x[:n] for x in held(cache, Layout(kb, vb, 0), 0))
+    for j in range(G):
+        qr = hadamard() @ q[0, j].double().cpu().numpy()
+        o = attention(qr, kh, vh, 1 / math.sqrt(D))
+        bound = output_bound(o, qr, kh, vh, 1 / math.sqrt(D), dtype)
+        bound = np.full(D, np.linalg.norm(bound)) + 2.0 ** -21 * np.linalg.norm(o)  # errors add up over the row
+        o = hadamard() @ o
+        bound = bound + np.abs(o) * torch.finfo(TYPES[dtype]).eps / 2
+        err = np.abs(out[0, j].double().cpu().numpy() - o)
+        assert (err <= bound).all()  # not-a-number fails
+
+
+def test_value_scales_at_the_ends_of_fp16_with_fp16_outputs():
+    # scales and zeros side by side over the whole type; outputs stay inside it
+    pool = Pool(11, 9, 1, 64, 4, 4, 0)
+    L = pool.lay
+    half = lambda x: np.asarray(x, np.float16).view(np.uint8)  # noqa: E731
+    n = pool.raw.shape[0] * 256
+    sc = np.random.RandomState(0).choice([0.0, 6e-8, 1e-5, 0.2, 900.0, 4000.0], n)
+    pool.raw[..., L.vs:L.vs + 512] = half(sc).reshape(pool.raw[..., L.vs:L.vs + 512].shape)
+    pool.cache.pages.copy_(torch.from_numpy(pool.raw.reshape(-1)))
+    _, check = decode_case(pool, 4, "f16", [513])
+    for j in range(4):
+        check(0, j)
