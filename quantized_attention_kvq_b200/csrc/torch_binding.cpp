@@ -96,10 +96,27 @@ int64_t row_stride(const at::Tensor& t, const char* name, int64_t heads) {
   return t.size(0) > 1 ? t.stride(0) : heads * 128;
 }
 
-void* stream_of(PyObject* o, int dev) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-  return reinterpret_cast<void*>(PyLong_AsUnsignedLongLong(o));
-}
+// The device and the stream of a call: the caller's, or the device's current one.  The
+// caller's is made current for the length of the call, so that memory allocated in it
+// belongs to the stream that uses it: a workspace given back on return goes to later work
+// of that stream only, and a new output is not still in use by another.
+class Place {
+ public:
+  Place(PyObject* o, int dev) : device_((c10::DeviceIndex)dev) {
+    if (o == Py_None) {
+      stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+      return;
+    }
+    stream = PyLong_AsVoidPtr(o);
+    if (PyErr_Occurred()) throw Refused();
+    stream_.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), (c10::DeviceIndex)dev));
+  }
+  void* stream;
+
+ private:
+  c10::cuda::CUDAGuard device_;
+  c10::cuda::OptionalCUDAStreamGuard stream_;
+};
 
 // A launch waits while the device's queue is full, an allocation may wait for the
 // device: neither holds up the process's other Python threads.
@@ -190,7 +207,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int dev = one_device({&ctx, &add, &table, &free_pages, &count, done});
     const int64_t sizes[5] = {n_slots, n_slots, B + 1, B, 1};
     const char* names[5] = {"slots", "positions", "cu_new", "seq_lens", "free_count"};
-    c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const Place on(a[10], dev);
     at::Tensor out[5], buf;
     int32_t* p[5];
     int64_t used = 0;
@@ -210,7 +227,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     call("kvq_page_plan", f_plan, num_pages, page_tokens, (int32_t)B, ints(&ctx, "ctx_lens", {B}),
          ints(&add, "new_lens", {B}), ints(done, "done", {B}), ints(&table, "block_table", {B, max_pages}),
          (int32_t)max_pages, ints(&free_pages, "free_pages", {num_pages}), ints(&count, "free_count", {1}), p[4], p[0],
-         p[1], n_slots, p[2], p[3], stream_of(a[10], dev));
+         p[1], n_slots, p[2], p[3], on.stream);
     if (a[9] != Py_None) {
       Py_INCREF(a[9]);
       return a[9];
@@ -232,9 +249,9 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t ks = row_stride(k, "k_new", H), vs = row_stride(v, "v_new", H), rows = k.size(0);
     const int32_t* at_slots = ints(&slots, "slots", {rows});
     if (rows > INT32_MAX) refuse("k_new has too many rows");
-    c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const Place on(a[6], dev);
     call("kvq_paged_append", f_append, reinterpret_cast<const kvq_paged_cache*>(integer(a[0])), k.data_ptr(), ks,
-         v.data_ptr(), vs, type_of(k.scalar_type(), "k_new"), (int32_t)rows, at_slots, stream_of(a[6], dev));
+         v.data_ptr(), vs, type_of(k.scalar_type(), "k_new"), (int32_t)rows, at_slots, on.stream);
     Py_RETURN_NONE;
   });
 }
@@ -250,11 +267,11 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* at_slots = ints(&slots, "slots", {rows});
     if (rows > INT32_MAX) refuse("slots has too many entries");
     const at::ScalarType type = code == KVQ_F32 ? at::kFloat : code == KVQ_BF16 ? at::kBFloat16 : at::kHalf;
-    c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const Place on(a[8], dev);
     const int64_t shape[3] = {rows, H, 128};
     at::Tensor k = output(k_out, "k_out", shape, type, dev), v = output(v_out, "v_out", shape, type, dev);
     call("kvq_paged_gather", f_gather, reinterpret_cast<const kvq_paged_cache*>(integer(a[0])), at_slots, (int32_t)rows,
-         (kvq_dtype)code, integer32(a[5], "rotate_back"), k.data_ptr(), v.data_ptr(), stream_of(a[8], dev));
+         (kvq_dtype)code, integer32(a[5], "rotate_back"), k.data_ptr(), v.data_ptr(), on.stream);
     PyObject* t = PyTuple_New(2);
     if (!t) throw Refused();
     PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(k));
@@ -280,7 +297,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t *p_table = ints(&table, "block_table", {B, max_pages}), *p_lens = ints(&lens, "seq_lens", {B});
     const int32_t* p_mask = ints(mask, "mask", {B, H});
     if (B > INT32_MAX || Hq > INT32_MAX || max_pages > INT32_MAX) refuse("q or block_table is too large");
-    c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const Place on(a[11], dev);
     const int64_t shape[3] = {B, Hq, 128};
     at::Tensor o = output(out, "out", shape, q.scalar_type(), dev);
     at::Tensor own;
@@ -292,7 +309,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     call("kvq_paged_decode", f_decode, desc, q.data_ptr(), stride, type, (int32_t)Hq, (int32_t)B, p_table,
          (int32_t)max_pages, p_lens, integer32(a[6], "max_len"), reinterpret_cast<const uint32_t*>(p_mask), (float)scale,
-         o.data_ptr(), ws->data_ptr(), ws->nbytes(), stream_of(a[11], dev));
+         o.data_ptr(), ws->data_ptr(), ws->nbytes(), on.stream);
     return THPVariable_Wrap(o);
   });
 }

@@ -56,3 +56,66 @@ def test_value_scales_at_the_ends_of_fp16_with_fp16_outputs():
     _, check = decode_case(pool, 4, "f16", [513])
     for j in range(4):
         check(0, j)
+
+
+# ------------------------------------------------------------- a caller's stream
+def new_segments(call):
+    """Streams of the memory the allocator takes from the device during a call."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = {x["address"] for x in torch.cuda.memory_snapshot()}
+    call()  # what it returned is given back, but stays the allocator's
+    return [x["stream"] for x in torch.cuda.memory_snapshot() if x["address"] not in before]
+
+
+def test_memory_made_for_a_call_on_a_given_stream_belongs_to_that_stream():
+    # sizes over the allocator's shared small blocks, so that each call takes memory of its own
+    B, H, G, P, num = 512, 8, 4, 64, 64
+    cache = native.PagedKVQCache(num, H, 4, 4, page_tokens=P)
+    q = torch.randn(B, H * G, D, device="cuda", dtype=torch.bfloat16)
+    table, lens = i32(np.arange(2 * B).reshape(B, 2) % num), i32(np.full(B, 100))
+    n = 1 << 20
+    zeros, ones = i32(np.zeros(B)), i32(np.ones(B))
+    free, count, slots = i32(np.arange(num)), i32([num]), i32(np.arange(4096) % (num * P))
+    side = torch.cuda.Stream()
+    out = torch.empty_like(q)
+    calls = [lambda: cache.decode(q, table, lens, 128, stream=side),
+             lambda: cache.decode(q, table, lens, 128, out=out, stream=side),  # the workspace alone
+             lambda: cache.gather(slots, torch.float32, stream=side),
+             lambda: cache.planner.plan(zeros, ones, table, free, count, n, stream=side).slots]
+    main = torch.cuda.current_stream()
+    for call in calls:
+        streams = new_segments(call)
+        assert streams and all(s == side.cuda_stream for s in streams)
+        assert torch.cuda.current_stream() == main  # as it was
+    for call in (lambda: cache.decode(q, table, lens, 128), lambda: cache.gather(slots, torch.float32)):
+        streams = new_segments(call)
+        assert streams and all(s == main.cuda_stream for s in streams)
+
+
+def test_decodes_on_a_given_stream_beside_allocations_on_the_current_one():
+    pool = Pool(13, 60, 2, 64, 4, 4, 0)
+    B, Hq = 6, 8
+    table, lens = i32(np.random.RandomState(1).permutation(60).reshape(B, 10)), i32([640, 100, 7, 333, 64, 0])
+    q = torch.randn(B, Hq, D, device="cuda", dtype=torch.bfloat16)
+    ref = pool.cache.decode(q, table, lens, 640)
+    side = torch.cuda.Stream()
+    words = pool.cache.workspace_bytes(B, Hq) // 4
+    torch.cuda.synchronize()
+    outs, fills = [], []
+    for i in range(60):
+        outs.append(pool.cache.decode(q, table, lens, 640, stream=side))
+        fills.append(torch.full((words,), float(i), device="cuda"))
+        if i % 7 == 6:
+            assert all(bool((f == j + 7 * (i // 7)).all()) for j, f in enumerate(fills))
+            fills = []
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
+
+
+@pytest.mark.parametrize("stream", ["x", 1.5])
+def test_a_stream_that_is_none_is_refused(stream):
+    cache = native.PagedKVQCache(2, 1, 4, 4)
+    fast = native._binding()
+    with pytest.raises((TypeError, ValueError)):
+        fast.gather(cache._at, cache.H, cache._dev, i32([0]), native.KVQ_F32, 0, None, None, stream)
