@@ -161,6 +161,15 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+def _empty(stream, shape, dtype: torch.dtype, device) -> torch.Tensor:
+    """New memory for a call on `stream`: it belongs to that stream, so that it goes to later work of no
+    other one when it is given back."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def describe(B, H, capacity, k_bits, v_bits, rotate_k=1, keep_ch0=0, d=128, rotate_v=0, v_clip=1.0, sink=0,
              recent=0) -> KvqCacheStruct:
     d_ = KvqCacheStruct(B, H, d, capacity, k_bits, v_bits, 32, 4, rotate_k, keep_ch0, rotate_v, v_clip)
@@ -260,7 +269,7 @@ class KVQCache:
     def select(self, q: torch.Tensor, keep_groups: int, mask_out: torch.Tensor | None = None, stream=None):
         """q: [B][Hq][128]; returns mask [B][H] (int32 tensor holding uint32 bits)."""
         if mask_out is None:
-            mask_out = torch.empty((self.B, self.H), dtype=torch.int32, device=q.device)
+            mask_out = _empty(stream, (self.B, self.H), torch.int32, q.device)
         _check(lib().kvq_select_channels(ctypes.byref(self.desc), _dev_ptr(q), torch_dtype_code(q.dtype),
                                          q.shape[1], keep_groups, _dev_ptr(mask_out), _stream(stream)),
                "kvq_select_channels")
@@ -271,7 +280,7 @@ class KVQCache:
         """Selection for queries at positions seq_lens - 1; returns mask [B][nb][H]
         (nb buckets, 1 without bucket-relative RoPE)."""
         if mask_out is None:
-            mask_out = torch.empty((self.B, self.n_buckets, self.H), dtype=torch.int32, device=q.device)
+            mask_out = _empty(stream, (self.B, self.n_buckets, self.H), torch.int32, q.device)
         _check(lib().kvq_select_channels_at(ctypes.byref(self.desc), _dev_ptr(q), torch_dtype_code(q.dtype),
                                             q.shape[1], _dev_ptr(seq_lens), keep_groups, _dev_ptr(mask_out),
                                             _stream(stream)),
@@ -290,9 +299,9 @@ class KVQCache:
         if softmax_scale is None:
             softmax_scale = 1.0 / math.sqrt(128)
         if out is None:
-            out = torch.empty((self.B, Hq, 128), dtype=torch.float32, device=q.device)
+            out = _empty(stream, (self.B, Hq, 128), torch.float32, q.device)
         if workspace is None:
-            workspace = torch.empty(max(self.workspace_bytes(Hq, max_len), 256), dtype=torch.uint8, device=q.device)
+            workspace = _empty(stream, max(self.workspace_bytes(Hq, max_len), 256), torch.uint8, q.device)
         _check(lib().kvq_decode_attention(ctypes.byref(self.desc), _dev_ptr(q), torch_dtype_code(q.dtype), Hq,
                                           _dev_ptr(seq_lens), max_len, _dev_ptr(mask), float(softmax_scale),
                                           _dev_ptr(out), _dev_ptr(workspace), workspace.numel(), _stream(stream)),
@@ -314,9 +323,9 @@ class KVQCache:
         if softmax_scale is None:
             softmax_scale = 1.0 / math.sqrt(128)
         if out is None:
-            out = torch.empty((self.B, Hq, 128), dtype=torch.float32, device=q.device)
+            out = _empty(stream, (self.B, Hq, 128), torch.float32, q.device)
         if workspace is None:
-            workspace = torch.empty(max(self.workspace_bytes(Hq, max_len), 256), dtype=torch.uint8, device=q.device)
+            workspace = _empty(stream, max(self.workspace_bytes(Hq, max_len), 256), torch.uint8, q.device)
         _check(lib().kvq_decode_attention_select(ctypes.byref(self.desc), _dev_ptr(q), torch_dtype_code(q.dtype), Hq,
                                                  _dev_ptr(seq_lens), max_len, keep_groups, float(softmax_scale),
                                                  _dev_ptr(out), _dev_ptr(workspace), workspace.numel(),
@@ -487,7 +496,7 @@ class PagedKVQCache:
         if q.dim() != 3 or q.shape[2] != 128 or not q.is_contiguous():
             raise ValueError("q is a contiguous [B][Hq][128]")
         if mask_out is None:
-            mask_out = torch.empty((q.shape[0], self.H), dtype=torch.int32, device=q.device)
+            mask_out = _empty(stream, (q.shape[0], self.H), torch.int32, q.device)
         d = describe(q.shape[0], self.H, 128, self.desc.k_bits, self.desc.v_bits, self.desc.rotate_k,
                      self.desc.keep_ch0)
         _call(dev, stream, "kvq_select_channels", lib().kvq_select_channels, ctypes.byref(d), q.data_ptr(),

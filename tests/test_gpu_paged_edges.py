@@ -113,6 +113,22 @@ def test_decodes_on_a_given_stream_beside_allocations_on_the_current_one():
     assert all(torch.equal(o, ref) for o in outs)
 
 
+def test_selections_and_contiguous_decodes_on_a_given_stream_use_memory_of_that_stream():
+    B, H, G, T = 64, 8, 4, 1024
+    cache = native.KVQCache(B, H, T, 4, 4)
+    paged = native.PagedKVQCache(4, 4096, 4, 4)
+    q = torch.randn(B, H * G, D, device="cuda", dtype=torch.bfloat16)
+    wide = torch.randn(128, 4096, D, device="cuda", dtype=torch.bfloat16)
+    lens = i32(np.full(B, T))
+    mask, out = cache.select(q, 20), torch.empty(B, H * G, D, device="cuda")
+    side = torch.cuda.Stream()
+    for call in (lambda: cache.decode(q, lens, T, stream=side), lambda: cache.decode(q, lens, T, mask, out=out, stream=side),
+                 lambda: cache.decode_select(q, lens, T, 20, stream=side), lambda: cache.select(q, 20, stream=side),
+                 lambda: cache.select_at(q, lens, 20, stream=side), lambda: paged.select(wide, 20, stream=side)):
+        streams = new_segments(call)
+        assert streams and all(s == side.cuda_stream for s in streams)
+
+
 @pytest.mark.parametrize("stream", ["x", 1.5])
 def test_a_stream_that_is_none_is_refused(stream):
     cache = native.PagedKVQCache(2, 1, 4, 4)
