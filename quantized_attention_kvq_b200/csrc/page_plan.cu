@@ -224,11 +224,29 @@ __global__ void __launch_bounds__(TH) k_page_plan(PlanArgs a) {
 
 }  // namespace
 
+static size_t plan_smem(int batch) { return sizeof(int) * (4 * (size_t)batch + 3); }
+
+// The limit is the function's, not a call's: it is set once per device, to what the
+// largest batch needs, and never lowered under another thread's launch
+template <int TH>
+static cudaError_t allow_smem() {
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev > 63 || !(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(k_page_plan<TH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem(kMaxPlanBatch));
+    if (e == cudaSuccess && dev <= 63) ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return e;
+}
+
 template <int TH>
 static cudaError_t launch_sized(const PlanArgs& a, int ctas, cudaStream_t s) {
-  const size_t smem = sizeof(int) * (4 * (size_t)a.batch + 3);
+  const size_t smem = plan_smem(a.batch);
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(k_page_plan<TH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem<TH>();
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -255,16 +273,15 @@ static int plan_ctas() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return kPortable;
   int n = known[dev].load(std::memory_order_relaxed);
   if (n) return n;
-  const int smem = (int)sizeof(int) * (4 * kMaxPlanBatch + 3);
   int clusters = 0;
   n = kPortable;
   if (cudaFuncSetAttribute(k_page_plan<1024>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-      cudaFuncSetAttribute(k_page_plan<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess) {
+      allow_smem<1024>() == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
     cfg.gridDim = dim3(kWidest);
     cfg.blockDim = dim3(1024);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = plan_smem(kMaxPlanBatch);
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = kWidest;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;

@@ -135,3 +135,31 @@ def test_a_stream_that_is_none_is_refused(stream):
     fast = native._binding()
     with pytest.raises((TypeError, ValueError)):
         fast.gather(cache._at, cache.H, cache._dev, i32([0]), native.KVQ_F32, 0, None, None, stream)
+
+
+# ------------------------------------------------------------- planning
+def test_plans_of_two_threads_with_batches_of_different_size():
+    # each batch asks for its own amount of shared memory (over 48 KB); neither call may narrow the other's
+    import threading
+    failed = []
+
+    def work(B, stream):
+        try:
+            torch.cuda.set_device(0)
+            p = native.PagePlanner(4 * B, 64)
+            args = [i32(np.zeros(B)), i32(np.ones(B)), i32(np.full((B, 2), -1)), i32(np.arange(4 * B)), i32([4 * B])]
+            out = native.PagePlan(*(torch.zeros(m, dtype=torch.int32, device="cuda") for m in (B, B, B + 1, B, 1)))
+            torch.cuda.synchronize()
+            for _ in range(3000):
+                p.plan(*args, B, out=out, stream=stream)
+            stream.synchronize()
+            assert int(out.free_count) == 3 * B and out.seq_lens.eq(1).all()
+        except Exception as e:  # noqa: BLE001
+            failed.append((B, e))
+
+    threads = [threading.Thread(target=work, args=(B, torch.cuda.Stream())) for B in (8192, 3100, 5000, 4000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
