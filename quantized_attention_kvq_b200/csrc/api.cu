@@ -20,7 +20,7 @@ kvq_status check_shape(const kvq_cache* c) {
   if ((c->rotate_v != 0 && c->rotate_v != 1) || !(c->v_clip > 0.0f && c->v_clip <= 1.0f)) return KVQ_ERR_INVALID_ARG;
   if (c->sink_tokens < 0 || c->recent_tokens < 0 || (int64_t)c->sink_tokens + c->recent_tokens > c->capacity)
     return KVQ_ERR_INVALID_ARG;
-  if (c->sink_tokens + c->recent_tokens > 2048) return KVQ_ERR_UNSUPPORTED;  // the window kernel's shared memory
+  if (c->sink_tokens + c->recent_tokens > kMaxWindow) return KVQ_ERR_UNSUPPORTED;  // the window kernel's shared memory
   if (c->head_dim != kHeadDim || c->group_size != kGroup || c->prune_granule != kGranule) return KVQ_ERR_UNSUPPORTED;
   if ((c->k_bits != 2 && c->k_bits != 4) || (c->v_bits != 2 && c->v_bits != 4)) return KVQ_ERR_UNSUPPORTED;
   if (c->capacity % kKeyBlock != 0) return KVQ_ERR_UNSUPPORTED;

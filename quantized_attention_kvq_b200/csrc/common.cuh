@@ -11,6 +11,7 @@
 namespace kvq {
 
 constexpr int kHeadDim = 128;
+constexpr int kMaxWindow = 2048;  // bf16 window tokens of a sequence
 constexpr int kGroup = 32;         // channels per quantization group
 constexpr int kGroups = kHeadDim / kGroup;      // 4
 constexpr int kGranule = 4;        // channels per pruning group

@@ -173,15 +173,21 @@ __global__ void __launch_bounds__(kWinThreads) k_window(DecodeArgs a) {
   }
 }
 
+// nq: query sets (bucket-relative RoPE: up to three buckets)
+constexpr size_t window_smem(int G, int nq, int ws) {
+  return (size_t)(nq * G * kHeadDim + G * ws + G * kWinWarps + ws + (kWinParts - 1) * G * kHeadDim) * sizeof(float);
+}
+
 template <int G>
 cudaError_t launch_window_g(const DecodeArgs& a, cudaStream_t s) {
-  const int ws = a.c.sink + a.c.recent;
-  const int nq = a.bucket_nb > 0 ? 3 : 1;  // query sets (bucket-relative RoPE: up to three buckets)
-  const size_t smem =
-      (size_t)(nq * G * kHeadDim + G * ws + G * kWinWarps + ws + (kWinParts - 1) * G * kHeadDim) * sizeof(float);
+  const size_t smem = window_smem(G, a.bucket_nb > 0 ? 3 : 1, a.c.sink + a.c.recent);
   auto kern = a.dtype == KVQ_F32 ? k_window<G, float> : (a.dtype == KVQ_BF16 ? k_window<G, __nv_bfloat16> : k_window<G, __half>);
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the limit is the function's, not a call's: always the largest windows', so that no call
+    // lowers it under another thread's launch
+    constexpr size_t most = window_smem(G, 3, kMaxWindow);
+    static_assert(most <= 227 * 1024, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
   }
   kern<<<a.c.B * a.c.H, kWinThreads, smem, s>>>(a);
