@@ -437,7 +437,8 @@ KVQ_API size_t kvq_paged_bytes(const kvq_paged_cache* cache);
  *     cu_new[b] is request b's first index in it (cu_new[batch] the total,
  *     saturated at 2^31 - 1).  slots[n] and positions[n] of list entry n are
  *     the token's slot and its position in its request; -1 for tokens of
- *     unserved requests and for entries behind the list.
+ *     unserved requests and for entries behind the list.  A token of a served
+ *     request whose block-table entry is outside [0, num_pages) has slot -1.
  *  4. seq_lens_out[b] = ctx + new for served requests, else the cached length
  *     (so it tells which were served); *free_count_out the free pages left.
  * ctx_lens, new_lens: device int32 [batch]; done: device int32 [batch] or NULL;

@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(TH) k_page_plan(PlanArgs a) {
       if (!served) continue;
       if (pg >= 0)
         page = pg < held ? a.table[(size_t)b * a.max_pages + pg] : a.free_pages[top - 1 - (need[b] + pg - held)];
-      slot[k] = page * P + off;
+      slot[k] = (uint32_t)page < (uint32_t)a.num_pages ? page * P + off : -1;  // a table entry may be no page
       pos[k] = p;
       ++p;
       ++off;

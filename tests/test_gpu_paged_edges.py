@@ -163,3 +163,15 @@ def test_plans_of_two_threads_with_batches_of_different_size():
     for t in threads:
         t.join()
     assert not failed
+
+
+def test_plan_gives_no_slot_on_a_page_outside_the_pool():
+    # a served request whose partly filled page is none: its tokens on that page get slot -1 (their positions
+    # stand), wherever page * page_tokens lands in 32 bits; tokens on its other pages are as always
+    P, num = 64, 8
+    for bad in (-1, -2 ** 31, num, 1 << 26, (1 << 26) + 3, 2 ** 31 - 1):
+        table = i32([[bad, -1], [5, -1]])
+        p = native.PagePlanner(num, P).plan(i32([10, 10]), i32([60, 2]), table, i32([0, 1, 2, 3, 4, 6, 7, -1]), i32([7]), 70)
+        assert p.seq_lens.tolist() == [70, 12] and int(p.free_count) == 6
+        assert p.positions.tolist() == list(range(10, 70)) + [10, 11] + [-1] * 8
+        assert p.slots.tolist() == [-1] * 54 + [7 * P + i for i in range(6)] + [5 * P + 10, 5 * P + 11] + [-1] * 8, bad
