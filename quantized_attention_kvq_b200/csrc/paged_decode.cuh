@@ -240,6 +240,15 @@ __device__ __forceinline__ int rank_of(int tile, int ranks, int total) {
   return tile < cut ? tile / (base + 1) : more + (tile - cut) / base;
 }
 
+// The power of two that value scales up to smax are multiplied with, so that P' = p *
+// scale keeps its low end: 1 for scales of 2^-6 to 2^6, beyond that what takes smax to
+// [1/2, 1).  Without it the p that fp16 holds above its subnormals would span as many
+// powers of two fewer as the scales are small, and a long tail of small p be lost.
+__device__ __forceinline__ float scales_up(float smax) {
+  if (smax == 0.0f || (smax >= 0.015625f && smax <= 64.0f)) return 1.0f;
+  return __int_as_float((253 - min(__float_as_int(smax) >> 23, 200)) << 23);
+}
+
 // One tile of a warp's range, as its lanes leave it in shared memory (16 bytes)
 struct Tile {
   int block;     // its block's number in the pool, -1: the page is outside the pool
@@ -472,7 +481,9 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
   // zero-point sums: per group and head of the thread's own tokens (fp32), or
   // as the product with the zeros leaves them (rows: groups)
   float zs[kGroups][HT], zp[NH][4];
-  float smax = 0.0f, plim = kTop16;  // largest value scale met, bound of p that keeps P' in fp16
+  // largest value scale met, power of two that takes scales to fp16's middle (P' and O
+  // carry it), bound of p that keeps P' in fp16
+  float smax = 0.0f, up = 1.0f, plim = kTop16;
 
   constexpr int kTop = PREC ? 6 : 14;
   constexpr float kUp = 1.0f / S::LOW;
@@ -605,6 +616,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
     }
     __syncwarp();
     smax = 0.0f;
+    up = 1.0f;
     plim = kTop16;
 #pragma unroll
     for (int k = 0; k < HT; ++k) {
@@ -648,7 +660,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
         }
       }
     }
-    constexpr float kOne = 1.0f / kCode;
+    const float one = 1.0f / (kCode * up);
 #pragma unroll
     for (int k = 0; k < HT; ++k) {
       const int hd = head_of(k);
@@ -663,10 +675,10 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
         const float r0 = HC == 4 ? O[m][0] : O[m][4 * (k >> 1) + (k & 1)];
         const float r1 = HC == 4 ? O[m][1] : O[m][4 * (k >> 1) + 2 + (k & 1)];
         if (VB == 4) {
-          float2 v = make_float2(fmaf(r0, kOne, zs[m >> 1][k]), fmaf(r1, kOne / 16.0f, zs[m >> 1][k]));
+          float2 v = make_float2(fmaf(r0, one, zs[m >> 1][k]), fmaf(r1, one * 0.0625f, zs[m >> 1][k]));
           *reinterpret_cast<float2*>(dst + 16 * m + 2 * g) = v;
         } else {
-          const float s0 = (m & 1) ? kOne / 16.0f : kOne, s1 = (m & 1) ? kOne / 64.0f : kOne / 4.0f;
+          const float s0 = (m & 1) ? one * 0.0625f : one, s1 = (m & 1) ? one * 0.015625f : one * 0.25f;
           float2 v = make_float2(fmaf(r0, s0, zs[m >> 1][k]), fmaf(r1, s1, zs[m >> 1][k]));
           *reinterpret_cast<float2*>(dst + 32 * (m >> 1) + 4 * g + 2 * (m & 1)) = v;
         }
@@ -852,8 +864,14 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
         if (__any_sync(kFull, over)) {
 #pragma unroll
           for (int m = 1; m < 32; m <<= 1) tile_scale = fmaxf(tile_scale, __shfl_xor_sync(kFull, tile_scale, m));
-          if (tile_scale > smax) smax = 1.25f * tile_scale;  // the next largest ones do not come back here
-          plim = kTop16 / fmaxf(smax, 1.0f);
+          float turn = 1.0f;  // of the sums so far, to the new power
+          if (tile_scale > smax) {
+            smax = 1.25f * tile_scale;  // the next largest ones do not come back here
+            const float next = scales_up(smax);
+            turn = __int_as_float(__float_as_int(next) - __float_as_int(up) + (127 << 23));
+            up = next;
+          }
+          plim = kTop16 / fmaxf(smax * up, 1.0f);
           const float room = __log2f(plim) - 8.0f;  // the largest p becomes plim / 2^8
 #pragma unroll
           for (int k = 0; k < HT; ++k) {
@@ -873,14 +891,15 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
               zp[k >> 1][k & 1] *= al;
               zp[k >> 1][2 + (k & 1)] *= al;
             }
+            const float ao = al * turn;
 #pragma unroll
             for (int m = 0; m < 8; ++m) {
               if (HC == 4) {
-                O[m][0] *= al;
-                O[m][1] *= al;
+                O[m][0] *= ao;
+                O[m][1] *= ao;
               } else {
-                O[m][4 * (k >> 1) + (k & 1)] *= al;
-                O[m][4 * (k >> 1) + 2 + (k & 1)] *= al;
+                O[m][4 * (k >> 1) + (k & 1)] *= ao;
+                O[m][4 * (k >> 1) + 2 + (k & 1)] *= ao;
               }
             }
 #pragma unroll
@@ -950,6 +969,27 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
           }
         }
         // ================================================================ value sums
+        if (up != 1.0f) {  // the same in all lanes
+          if (PREC) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int k = 0; k < HT; ++k) p[i][e][k] *= up;
+          } else {  // in two steps: the power itself may be outside fp16
+            const int ex = (__float_as_int(up) >> 23) - 127;
+            const float u0 = __int_as_float((127 + (ex >> 1)) << 23), u1 = __int_as_float((127 + ex - (ex >> 1)) << 23);
+            const uint32_t h0 = half2_of(u0, u0), h1 = half2_of(u1, u1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              vs[i].x = hmul2(hmul2(vs[i].x, h0), h1);
+              vs[i].y = hmul2(hmul2(vs[i].y, h0), h1);
+              vs[i].z = hmul2(hmul2(vs[i].z, h0), h1);
+              vs[i].w = hmul2(hmul2(vs[i].w, h0), h1);
+            }
+          }
+        }
         constexpr int NR = S::PAIR ? 2 : 4;  // rounds: a pair of groups or one group each
 #pragma unroll
         for (int rd = 0; rd < NR; ++rd) {

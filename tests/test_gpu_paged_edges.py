@@ -175,3 +175,44 @@ def test_plan_gives_no_slot_on_a_page_outside_the_pool():
         assert p.seq_lens.tolist() == [70, 12] and int(p.free_count) == 6
         assert p.positions.tolist() == list(range(10, 70)) + [10, 11] + [-1] * 8
         assert p.slots.tolist() == [-1] * 54 + [7 * P + i for i in range(6)] + [5 * P + 10, 5 * P + 11] + [-1] * 8, bad
+
+
+# ------------------------------------------------------------- small values
+@pytest.mark.parametrize("vb", [4, 2])
+@pytest.mark.parametrize("std", [2e-4, 5e-5, 2e-6, 4000.0])
+@pytest.mark.parametrize("G,dtype", [(4, "bf16"), (8, "bf16"), (4, "f16"), (16, "f16"), (4, "f32"), (8, "f32")])
+def test_decode_accuracy_does_not_depend_on_the_values_magnitude(vb, std, G, dtype):
+    # one token holds some 3/4 of the weight, 131071 others share the rest: products of their
+    # probabilities and scales span 2^-19 below the largest, wherever the scales lie.  As many
+    # requests as the decode has warps, over the same pages: a request is not cut into short pieces
+    num, P, n, B = 32, 4096, 131072, 148 * 16
+    pool = Pool(3, 1, 1, 64, 4, vb, 0, rot=0)
+    L = pool.lay
+    r = np.random.RandomState(int(1e7 * std) % 1000 + vb)
+    raw = np.zeros((num * P // BT, L.bytes), np.uint8)
+    half = lambda x: np.asarray(x).astype(np.float16).view(np.uint8)  # noqa: E731
+    raw[:, L.vc:L.vs] = r.randint(0, 256, (len(raw), L.vs - L.vc))
+    step = 4 * std / ((1 << vb) - 1)
+    raw[:, L.vs:L.vs + 512] = half(step * r.uniform(0.8, 1.2, (len(raw), 256)))
+    raw[:, L.vz:L.vz + 512] = half(-2 * std * r.uniform(0.5, 1.5, (len(raw), 256)))
+    top = 4097  # the token with the weight: its keys are constants, all others zero
+    for grp in range(4):
+        at = L.kz + L.tables()["kz"][top % BT, grp]
+        raw[top // BT, at:at + 2] = half([13.0 / 128 * math.sqrt(D)])
+    raw = raw.reshape(num, 1, P // BT, L.bytes)
+    cache = native.PagedKVQCache(num, 1, 4, vb, page_tokens=P, rotate_k=0)
+    cache.pages.copy_(torch.from_numpy(raw.reshape(-1)))
+    kh, vh = held(cache, L, 0)
+    q = torch.ones(B, G, D, device="cuda", dtype=TYPES[dtype])
+    out = cache.decode(q, i32(np.tile(np.arange(num), (B, 1))), i32(np.full(B, n)), n)
+    o = attention(np.ones(D), kh, vh, 1 / math.sqrt(D))
+    bound = output_bound(o, np.ones(D), kh, vh, 1 / math.sqrt(D), dtype)
+    if dtype == "f16":
+        bound = bound + 2.0 ** -25  # half a step of the type's subnormals
+    if dtype == "f32":  # a lane adds its 8 tokens of a tile one after another, n / 8 sums that are each off by up
+        # to 2^-24 of what they hold, in the numerator and in the divisor
+        bound = bound + 2 * (n / 8) * 2.0 ** -24 * np.abs(vh).max()
+    for b in (0, 1, B // 2, B - 1):
+        for j in range(G):
+            err = np.abs(out[b, j].double().cpu().numpy() - o)
+            assert (err <= bound).all(), (b, j, float((err / bound).max()))
