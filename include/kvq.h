@@ -458,10 +458,7 @@ KVQ_API kvq_status kvq_page_plan(int32_t num_pages, int32_t page_tokens, int32_t
 
 /*
  * Quantize n tokens' keys and values into their slots, with the arithmetic of
- * kvq_quantize_append except that scale = fp16((max - min) * fp32(1 / L)): the
- * product is within one unit in the last place of the quotient, so scales and
- * codes are the same bits but for the few groups (under 1 in 10,000) whose
- * quotient lies that close to the middle of two fp16 numbers.
+ * kvq_quantize_append: the same scales, zeros, codes and channel 0, bit for bit.
  *  k_new, v_new: device rows of `dtype`, token t's head h at element
  *  t * k_stride + h * 128 (t * v_stride + h * 128), e.g. slices of a fused
  *  projection; strides in elements, at least kv_heads * 128, bases and row

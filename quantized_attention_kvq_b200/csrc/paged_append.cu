@@ -2,8 +2,8 @@
 //
 // A warp takes 8 tokens of one head's keys (or values), four lanes per token,
 // lane g owning the 32 channels of quantization group g: fp64 Walsh-Hadamard
-// butterflies and the quantizer of the contiguous append (the scale by a
-// reciprocal instead of a division).  Keys and values are separate blocks of the
+// butterflies and the quantizer of the contiguous append: the same bits for the same
+// tokens.  Keys and values are separate blocks of the
 // grid: twice the parallelism in a decode step's small append, and half the
 // registers.
 //

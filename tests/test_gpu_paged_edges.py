@@ -216,3 +216,23 @@ def test_decode_accuracy_does_not_depend_on_the_values_magnitude(vb, std, G, dty
         for j in range(G):
             err = np.abs(out[b, j].double().cpu().numpy() - o)
             assert (err <= bound).all(), (b, j, float((err / bound).max()))
+
+
+# ------------------------------------------------------------- one definition of the scale
+@pytest.mark.parametrize("kb,vb,rot,ch0,rotv,clip,dtype", [(4, 4, 1, 0, 0, 1.0, "bf16"), (2, 4, 0, 1, 1, 0.92, "f32"),
+                                                           (4, 2, 1, 1, 0, 0.9, "f16")])
+def test_append_of_many_rows_holds_the_oracles_values_in_every_row(kb, vb, rot, ch0, rotv, clip, dtype):
+    # the oracle's scale is the quotient (max - min) / L, which some 84 of a million 4-bit groups tell from a
+    # product with 1 / L; rows next to a rounding boundary are no exception
+    from test_gpu_paged import oracle_cache, rows
+    n, H, P = 16384, 8, 256
+    cache = native.PagedKVQCache(n // P, H, kb, vb, page_tokens=P, rotate_k=rot, keep_ch0=ch0, rotate_v=rotv, v_clip=clip)
+    k, v = rows(31, n, H, dtype)
+    slots = i32(np.random.RandomState(1).permutation(n))
+    cache.append(k, v, slots)
+    kd, vd = cache.gather(slots, torch.float32, rotate_back=False)
+    oc = oracle_cache(k, v, kb, vb, rot, ch0, rotv, clip)
+    for h in range(H):
+        kh, vh = oc.dequantize(0, h, 0, n)
+        for got, want in ((kd, kh), (vd, vh)):
+            assert np.array_equal(got[:, h].cpu().numpy(), want.astype(np.float32)), h
