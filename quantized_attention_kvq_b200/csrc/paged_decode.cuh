@@ -37,8 +37,9 @@
 //           in-register 8x8 transpose; no shared memory is written.
 // Softmax: p = 2^(s - M) with M raised only when p or p * scale could pass 2^15
 // (bounds kept per warp), so both fit fp16 and one warp vote per tile usually
-// replaces the maxima.  p is rounded to fp16 once; P' and the zero-point sums,
-// one more product with the transposed zeros, both start from it.  The sums over
+// replaces the maxima.  p is rounded to fp16 once; P', the zero-point sums, one more
+// product with the transposed zeros, and the divisor, a row of ones in it, all start from
+// it, so that the rounding of p is that of a weight and not of the output.  The sums over
 // a tile stay in the matrix unit's fp32 accumulators and are then added to fp32
 // registers, so a long sequence does not run up rounding in one direction.
 //
@@ -95,6 +96,10 @@ struct Shape {
   static constexpr bool PIECES = KB == 4 && HC == 4 && !PREC;
   static constexpr bool PAIR = HC == 4 && !PREC;  // P' columns: (head, group of a pair)
   static constexpr int OC = HC == 4 ? 2 : HC / 2;  // fp32 sums per thread and 16-channel tile
+  // whether the divisor is a product of its own with ones: for fp16 outputs no row of the
+  // zero-point product is free, and with 8 heads its registers are short (64 ragged
+  // requests, INT4 / INT2: 135 us against 138; 4 heads: no difference)
+  static constexpr bool ONES = MODE == kF16 || (MODE == kBf16 && HC == 8);
   static constexpr int WARPS = paged_decode_warps(HC, PREC);
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int QF = 8 * NT * 256;         // query fragments: 8 K-steps
@@ -642,14 +647,15 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
   auto end_segment = [&]() {
 #pragma unroll
     for (int k = 0; k < HT; ++k) {
+      if (PREC) {
 #pragma unroll
-      for (int m = 4; m < 32; m <<= 1) {
-        l[k] += __shfl_xor_sync(kFull, l[k], m);
-        if (PREC) {
+        for (int m = 4; m < 32; m <<= 1) {
+          l[k] += __shfl_xor_sync(kFull, l[k], m);
 #pragma unroll
           for (int r = 0; r < kGroups; ++r) zs[r][k] += __shfl_xor_sync(kFull, zs[r][k], m);
         }
       }
+      if (!PREC && !S::ONES) l[k] = __shfl_sync(kFull, zp[k >> 1][k & 1], 16 + cq);
       if (!PREC) {  // group r: row r (even tokens) and row 12 + r (odd ones) of the zeros' product
 #pragma unroll
         for (int r = 0; r < kGroups; ++r) {
@@ -915,7 +921,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
 #pragma unroll
             for (int k = 0; k < HT; ++k) {
               p[i][e][k] = x[i][e][k];
-              l[k] += x[i][e][k];
+              if (PREC) l[k] += x[i][e][k];
             }
         constexpr int kMid = S::MID;
         uint32_t ph[4][2][NH];  // p as fp16: the head twice (HC = 4), or a pair of heads
@@ -935,20 +941,31 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
           // where value and output do not (rotated values): the scales' sums are rows of their
           // own, in the places that are free: 4-7 the odd tokens', 8-11 the even ones'
           const uint4 vt = MODE == kF16 ? load_transposed(smem_addr(st + S::V_SCALES + 16 * lane)) : make_uint4(0, 0, 0, 0);
+          constexpr uint32_t kOnes = 0x3C003C00u;
           auto add_zeros = [&](float (&d)[4], int i, uint32_t b0, uint32_t b1) {
             const uint32_t zi = word(z, i), si = word(vt, i);
             if (MODE == kF16)
               mma16(d, g < 4 ? zi : 0u, g < 4 ? si : 0u, g < 4 ? 0u : si, g < 4 ? 0u : zi, b0, b1);
-            else
+            else if (S::ONES)
               mma16(d, zi, 0u, 0u, zi, b0, b1);
+            else  // row 4 sums the rounded p
+              mma16(d, g == 4 ? kOnes : zi, 0u, g == 4 ? kOnes : 0u, zi, b0, b1);
           };
 #pragma unroll
           for (int t = 0; t < NH; ++t) {
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dl[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) add_zeros(d, i, transpose8(ph[i][0][t]), transpose8(ph[i][1][t]));
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t b0 = transpose8(ph[i][0][t]), b1 = transpose8(ph[i][1][t]);
+              add_zeros(d, i, b0, b1);
+              if (S::ONES) mma16(dl, kOnes, kOnes, kOnes, kOnes, b0, b1);
+            }
 #pragma unroll
             for (int r = 0; r < 4; ++r) zp[t][r] += d[r];
+            if (S::ONES) {  // the same in all rows
+              l[(2 * t) % HT] += dl[0];
+              if (HC > 4) l[(2 * t + 1) % HT] += dl[1];
+            }
           }
         } else {
 #pragma unroll

@@ -236,3 +236,40 @@ def test_append_of_many_rows_holds_the_oracles_values_in_every_row(kb, vb, rot, 
         kh, vh = oc.dequantize(0, h, 0, n)
         for got, want in ((kd, kh), (vd, vh)):
             assert np.array_equal(got[:, h].cpu().numpy(), want.astype(np.float32)), h
+
+
+# ------------------------------------------------------------- probabilities
+@pytest.mark.parametrize("kb,vb", [(4, 4), (4, 2), (2, 2)])
+@pytest.mark.parametrize("G", [1, 4, 8, 16])
+@pytest.mark.parametrize("lens", [[1], [2, 7, 64, 65, 200]])
+def test_the_divisor_holds_the_same_rounded_probabilities_as_the_sums(kb, vb, G, lens):
+    # Value zeros near 1000 beside steps of some 3: an fp16 probability is off by up to 2^-11 of
+    # itself, but the sum with the zeros and the divisor take the same one, so what is left is
+    # P' = p * scale, 2^-11 of scale times the codes' distance from their middle, beside the final rounding.
+    pool = Pool(kb * 7 + vb, 16, 1, 64, kb, vb, 0)
+    L = pool.lay
+    half = lambda x: np.asarray(x, np.float16).view(np.uint8)  # noqa: E731
+    r = np.random.RandomState(5)
+    shape = pool.raw[..., L.vs:L.vs + 512].shape
+    m = shape[0] * 256
+    pool.raw[..., L.vs:L.vs + 512] = half(r.uniform(1.5, 3.5, m)).reshape(shape)
+    pool.raw[..., L.vz:L.vz + 512] = half(np.full(m, 1040.0)).reshape(shape)
+    pool.cache.pages.copy_(torch.from_numpy(pool.raw.reshape(-1)))
+    # scores: the fp32 sums' 2^-20 of |q| |k| scale, as in output_bound, times the values' spread about their mean
+    order = np.random.RandomState(17).permutation(16)
+    out, _ = decode_case(pool, G, "f16", lens, pad_pages=0)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q = torch.randn(len(lens), G, D, device="cuda", generator=g).half()
+    at = 0
+    for b, n in enumerate(lens):
+        pages = order[at:at + -(-n // 64)]
+        at += len(pages)
+        k, v = (x[:n] for x in pool.values(pages, 0))
+        for j in range(G):
+            qr = hadamard() @ q[b, j].double().cpu().numpy()
+            o = attention(qr, k, v, 1 / math.sqrt(D))
+            spread = np.ptp(v)
+            eps_s = 2.0 ** -20 * np.linalg.norm(qr) * np.linalg.norm(k, axis=1).max() / math.sqrt(D)
+            bound = np.abs(o) * (2.0 ** -11 + 2.0 ** -20) + 3.5 * (1 << (vb - 1)) * 2.0 ** -11 + 2 * eps_s * spread
+            err = np.abs(out[b, j].double().cpu().numpy() - o)
+            assert (err <= bound).all(), (b, j, float((err / bound).max()))
