@@ -389,16 +389,17 @@ def _i32(t: torch.Tensor | None, name: str, *shape: int) -> int | None:
     return t.data_ptr()
 
 
-def _call(dev: int, stream, what: str, fn, *args):
-    """One library call on the tensors' device, on its current stream or the caller's."""
+def _status_of(dev: int, stream, fn, *args) -> int:
+    """Status of one library call on the tensors' device, on its current stream or the caller's."""
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if dev == torch.cuda.current_device():
-        status = fn(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, raw)
-    if status != KVQ_OK:
-        raise KvqError(status, what)
+        return fn(*args, raw)
+    with torch.cuda.device(dev):
+        return fn(*args, raw)
+
+
+def _call(dev: int, stream, what: str, fn, *args):
+    _check(_status_of(dev, stream, fn, *args), what)
 
 
 _fast = None
@@ -517,5 +518,5 @@ class PagedKVQCache:
 
     def decode_status(self, batch: int, q_heads: int, workspace: torch.Tensor, stream=None) -> int:
         """Status of the last decode that used `workspace`: KVQ_OK or KVQ_ERR_TIMEOUT (synchronizes the stream)."""
-        return lib().kvq_paged_decode_status(self._ref, batch, q_heads, _dev_ptr(workspace),
-                                             workspace.nbytes, _stream(stream))
+        return _status_of(_device_of(workspace, self.pages), stream, lib().kvq_paged_decode_status, self._ref, batch, q_heads,
+                          _dev_ptr(workspace), workspace.nbytes)
