@@ -246,12 +246,14 @@ __device__ __forceinline__ int rank_of(int tile, int ranks, int total) {
 }
 
 // The power of two that value scales up to smax are multiplied with, so that P' = p *
-// scale keeps its low end: 1 for scales of 2^-6 to 2^6, beyond that what takes smax to
-// [1/2, 1).  Without it the p that fp16 holds above its subnormals would span as many
-// powers of two fewer as the scales are small, and a long tail of small p be lost.
+// scale and p both keep their low ends in fp16: 1 for scales of 2^-6 to 2^6.  Smaller ones
+// are taken to [1/2, 1): as they are, P' would span as many powers of two fewer above fp16's
+// subnormals as they are small, and a long tail of small p be lost.  Larger ones are taken to
+// [16, 32), which leaves p 10 of its 15 powers (the bound of p is 2^15 / scale) and small
+// scales beside a large one, whose p may be 0, 2^-18 of it before they are subnormal.
 __device__ __forceinline__ float scales_up(float smax) {
   if (smax == 0.0f || (smax >= 0.015625f && smax <= 64.0f)) return 1.0f;
-  return __int_as_float((253 - min(__float_as_int(smax) >> 23, 200)) << 23);
+  return __int_as_float(((smax < 1.0f ? 253 : 258) - min(__float_as_int(smax) >> 23, 200)) << 23);
 }
 
 // One tile of a warp's range, as its lanes leave it in shared memory (16 bytes)
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
   // zero-point sums: per group and head of the thread's own tokens (fp32), or
   // as the product with the zeros leaves them (rows: groups)
   float zs[kGroups][HT], zp[NH][4];
-  // largest value scale met, power of two that takes scales to fp16's middle (P' and O
+  // largest value scale met, power of two that the scales are multiplied with (P' and O
   // carry it), bound of p that keeps P' in fp16
   float smax = 0.0f, up = 1.0f, plim = kTop16;
 
@@ -878,7 +880,8 @@ __global__ void __launch_bounds__(Shape<KB, VB, HC, MODE, CH0>::THREADS, 1) k_pa
             up = next;
           }
           plim = kTop16 / fmaxf(smax * up, 1.0f);
-          const float room = __log2f(plim) - 8.0f;  // the largest p becomes plim / 2^8
+          // the largest p becomes plim / 2^8 (the room for later ones), but 2^6 where it can
+          const float room = fmaxf(__log2f(plim) - 8.0f, fminf(__log2f(plim) - 1.0f, 6.0f));
 #pragma unroll
           for (int k = 0; k < HT; ++k) {
             float t = -INFINITY;

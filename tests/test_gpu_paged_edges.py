@@ -179,7 +179,7 @@ def test_plan_gives_no_slot_on_a_page_outside_the_pool():
 
 # ------------------------------------------------------------- small values
 @pytest.mark.parametrize("vb", [4, 2])
-@pytest.mark.parametrize("std", [2e-4, 5e-5, 2e-6, 4000.0])
+@pytest.mark.parametrize("std", [2e-4, 5e-5, 2e-6, 150.0, 4000.0])
 @pytest.mark.parametrize("G,dtype", [(4, "bf16"), (8, "bf16"), (4, "f16"), (16, "f16"), (4, "f32"), (8, "f32")])
 def test_decode_accuracy_does_not_depend_on_the_values_magnitude(vb, std, G, dtype):
     # one token holds some 3/4 of the weight, 131071 others share the rest: products of their
@@ -213,6 +213,41 @@ def test_decode_accuracy_does_not_depend_on_the_values_magnitude(vb, std, G, dty
         # to 2^-24 of what they hold, in the numerator and in the divisor
         bound = bound + 2 * (n / 8) * 2.0 ** -24 * np.abs(vh).max()
     for b in (0, 1, B // 2, B - 1):
+        for j in range(G):
+            err = np.abs(out[b, j].double().cpu().numpy() - o)
+            assert (err <= bound).all(), (b, j, float((err / bound).max()))
+
+
+@pytest.mark.parametrize("vb", [4, 2])
+@pytest.mark.parametrize("G,dtype", [(4, "bf16"), (8, "bf16"), (16, "bf16"), (4, "f16"), (8, "f16"), (4, "f32")])
+@pytest.mark.parametrize("large,n", [(3000.0, 4), (60000.0, 4), (60000.0, 300)])
+def test_a_token_of_large_values_and_no_weight_takes_no_accuracy_from_the_others(vb, G, dtype, large, n):
+    # the token's score is some 60 nats below every other's: its weight is 0 in any of the types, and
+    # the outputs are those of the request without it (its own part, below 1e6 * e^-60, is nothing).
+    # As many requests as the decode has warps, over the same pages: each has one warp
+    P, B = 64, 148 * 16
+    L = Layout(4, vb, 0)
+    r = np.random.RandomState(vb)
+    raw = np.zeros((5, L.bytes), np.uint8)
+    half = lambda x: np.asarray(x).astype(np.float16).view(np.uint8)  # noqa: E731
+    raw[:, :L.ks] = r.randint(0, 256, (5, L.ks))
+    raw[:, L.ks:L.kz] = half(r.uniform(0.01, 0.03, (5, 256)))
+    raw[:, L.vc:L.vs] = r.randint(0, 256, (5, L.vs - L.vc))
+    raw[:, L.vs:L.vz] = half(r.uniform(0.02, 0.2, (5, 256)))
+    raw[:, L.vz:] = half(r.uniform(-1.0, -0.1, (5, 256)))
+    for grp in range(4):
+        at = L.vs + L.tables()["s"][2, grp]
+        raw[0, at:at + 2] = half([large])
+        at = L.kz + L.tables()["kz"][2, grp]
+        raw[0, at:at + 2] = half([-60.0 / 128 * math.sqrt(D)])
+    cache = native.PagedKVQCache(5, 1, 4, vb, page_tokens=P, rotate_k=0)
+    cache.pages.copy_(torch.from_numpy(raw.reshape(-1)))
+    kh, vh = (np.delete(x[:n], 2, 0) for x in held(cache, L, 0))
+    q = torch.ones(B, G, D, device="cuda", dtype=TYPES[dtype])
+    out = cache.decode(q, i32(np.tile(np.arange(5), (B, 1))), i32(np.full(B, n)), n)
+    o = attention(np.ones(D), kh, vh, 1 / math.sqrt(D))
+    bound = output_bound(o, np.ones(D), kh, vh, 1 / math.sqrt(D), dtype)
+    for b in (0, B // 2, B - 1):
         for j in range(G):
             err = np.abs(out[b, j].double().cpu().numpy() - o)
             assert (err <= bound).all(), (b, j, float((err / bound).max()))
