@@ -503,9 +503,15 @@ KVQ_API size_t kvq_paged_decode_workspace_bytes(const kvq_paged_cache* cache, in
  *        are not kept contribute nothing; INT4 keys with up to four query heads
  *        a kv head and 16-bit types do not read them either (elsewhere picking
  *        rows costs more time than their bytes).
- *  out:  device [batch][q_heads][128] of `dtype`.  For 16-bit types the
- *        probabilities are rounded to fp16 before the value sums; for fp32 they
- *        keep 22 bits.
+ *  out:  device [batch][q_heads][128] of `dtype`, which also says what is held
+ *        in fewer bits than 32.  For all types the query is rotated in fp32
+ *        (kvq_select_channels and the contiguous decode: fp64) and enters the
+ *        scores as two fp16 pieces (22 bits); scores, maxima and sums are fp32.
+ *        For 16-bit types the probabilities are rounded to fp16, alike in the
+ *        sums and in their divisor, their products with the value scales are
+ *        rounded to fp16 again, and the codes enter the products as fp16
+ *        subnormals (2^-18 of a score's largest product is lost).  For fp32 the
+ *        products keep 22 bits.
  *  workspace: device scratch, 256-byte aligned, not read by later calls (but
  *        two calls that may run at the same time need one each).
  */

@@ -134,14 +134,14 @@ struct PagedDecodeArgs {
   void* out;
   float* part_acc;   // [units + ranks][G][128] unnormalized sums
   float2* part_ml;   // [units + ranks][G] (running max, running sum)
-  int32_t* starts;   // [B + 1] first tile of each request, times H
+  int32_t* starts;   // [B + 1] tiles of one kv head before each request
   int32_t* status;   // [kPagedMaxRanks] 1 where a bounded wait of the rank gave up
   int withheld_tile; // test hook: rank 0 never fills this tile's ring slot (-1: none)
   size_t part_rows;
 };
 // The tiles of a decode are spread over ranks: the warps of one CTA per SM.  More
 // warps hide more latency, as long as their registers and rings fit: 8 heads a group
-// take 134 us with 12 warps and 146 with 14, a number the four schedulers cannot share
+// take 135 us with 12 warps, some 12 more with 14, a number the four schedulers cannot share
 // evenly (ragged batch of 64, INT4 / INT2).
 constexpr int kPagedSms = 148;
 constexpr int paged_decode_warps(int padded_heads, bool f32) {

@@ -7,11 +7,11 @@
 // grid: twice the parallelism in a decode step's small append, and half the
 // registers.
 //
-// Bound by instruction issue (54% of the slots, fp64 and its conversions a fifth of
-// that each) and by latencies at 20 warps a SM: 84 us for 32K tokens of 8 heads
-// (INT4 keys, INT2 values; 164 MB of input).  Tried and slower: writing words of
-// eight neighbouring tokens instead of bytes (92 us), persistent blocks that fetch
-// their next rows ahead (108 us).  A rotated row is loaded with its channels
+// Bound by latencies at 20 warps an SM (64 registers of doubles a lane): 54% of the issue
+// slots are used, the fp64 pipe 18%, conversions 22%, memory a quarter.  81 us for 32K
+// tokens of 8 heads (INT4 keys, INT2 values; 134 MB in, 30 MB out).  Tried and slower:
+// writing words of eight neighbouring tokens instead of bytes (8 us more), persistent
+// blocks that fetch their next rows ahead (24 us more).  A rotated row is loaded with its channels
 // interleaved over the four lanes, so that five of the seven stages stay in the
 // lane; one pass through shared memory (16-byte pieces, swizzled so that both
 // sides are free of bank conflicts) then brings lane g its own group, and the

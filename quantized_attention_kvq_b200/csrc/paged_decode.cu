@@ -88,7 +88,9 @@ __device__ __forceinline__ void finish_row(const PagedDecodeArgs& a, size_t row,
 // WPR warps per output row: one where a row has few partials (a block then takes
 // eight rows), eight where its sequence was cut into many: 16 ranks a unit or more
 // (us of the whole decode with one and eight: 296 units of 8 ranks 39 and 44; 128 of 18
-// 22.2 and 22.0; 64 of 37 67.8 and 62.8; 8 of 296 64 and 24).  A row's partials sit
+// 22.2 and 22.0; 64 of 37 67.8 and 62.8; 8 of 296 64 and 24).  The rule goes by the
+// average: one request of 128K tokens among 63 of 256 takes 76 us, one warp joining each of
+// the long request's rows of some 270 partials.  A row's partials sit
 // in slots unit + r of the ranks r its tiles touch, as the split cut them.
 template <int WPR>
 __global__ void __launch_bounds__(256) k_paged_join(PagedDecodeArgs a, int max_ranks) {

@@ -12,12 +12,15 @@
 // consecutive ranks in one CTA, which then joins its own units, 200 short requests
 // measured 44 us where interleaved ranks took 29).
 //
-// Measured on B200, both passes (of 6.55 TB/s measured): INT4, 8 x 32K tokens, 8 heads
-// of 4 queries 62 us (83%: memory); INT2 with channel 0, 4 x 128K 88-98 us (57%) and
-// INT4 / INT2, 64 ragged requests, 8 queries a head 125-139 us (55%): bound by
-// instruction issue (63% of the slots, ALU 58%, tensor pipe 43%; a third of the
-// instructions mask codes out of words); 200 requests of up to 700 tokens 25 us, of
-// which some 9 are the two launches' fixed part.
+// Measured on B200, per call in a stream of calls, both launches (of 6.55 TB/s measured):
+// INT4, 8 x 32K tokens, 8 heads of 4 queries 63 us (82%: memory); INT2 with channel 0, 4 x
+// 128K 94 us (58%; 61% of the issue slots, ALU 58%, tensor pipe 42%: a third of the
+// instructions mask codes out of words, and four warps a scheduler do not cover the waits
+// for them and for the products); INT4 / INT2, 64 ragged requests, 8 queries a head 135 us
+// (55%; 50% of the issue slots, three warps a scheduler waiting for dependent products); 200
+// requests of up to 700 tokens 26 us, of which some 9 are the two launches' fixed part.
+// Long fp32 decode (4 x 32K tokens, INT4) 48 us (53%), 16 queries a head (8 x 16K) 44 us (29%):
+// 8 warps an SM in both.
 //
 // Per tile, both products run on the tensor cores straight from the codes:
 //   scores  S^T = K Q^T: the key codes are the 16-row operand (16 tokens x 16
@@ -92,7 +95,8 @@ struct Shape {
   // 100 instructions a tile, so only where bytes are what a decode waits for.
   // INT4 keys and values, 4 heads a group, 32K tokens x 8: 54, 56 and 61 us with 8,
   // 20 and 28 of 32 groups kept against 64 for whole blocks; INT2 at 128K x 4: 94
-  // against 88 whatever is kept; INT4 / INT2 with 8 heads a group: 134 against 127.
+  // against 88 whatever is kept; INT4 / INT2 with 8 heads a group: 138, 138 and 140
+  // with 8, 16 and 24 kept against 132, 134 and 135.
   static constexpr bool PIECES = KB == 4 && HC == 4 && !PREC;
   static constexpr bool PAIR = HC == 4 && !PREC;  // P' columns: (head, group of a pair)
   static constexpr int OC = HC == 4 ? 2 : HC / 2;  // fp32 sums per thread and 16-channel tile

@@ -7,9 +7,9 @@
 // 24K tokens of 8 heads, INT4 to bf16 and back through the transform, 132 MB, 3.8
 // TB/s).  A lane reads its codes' bytes, forms scale * code + zero with one
 // rounding and takes the row back through the transform in fp32 when asked.
-// Bound by instruction issue (61%, most of it masks and shifts of codes) and by
-// the loads that follow the slot: 5.6 of the 13 cycles between two instructions of a
-// warp.
+// Bound by the loads that follow the slot, 5.7 of the 13 cycles between two instructions
+// of a warp, and by the ALU (66%: masks and shifts of codes); 63% of the issue slots are
+// used.
 #include "paged.cuh"
 
 namespace kvq {

@@ -433,7 +433,8 @@ class PagePlan:
 
 
 class PagePlanner:
-    """Block tables and slot maps of a page pool, built on the device (kvq_page_plan)."""
+    """Block tables and slot maps of a page pool, built on the device (kvq_page_plan).  New tensors that this
+    and the cache's calls return belong to the stream the call runs on (`stream`, or the current one)."""
 
     def __init__(self, num_pages: int, page_tokens: int = 64):
         self.num_pages, self.page_tokens = num_pages, page_tokens

@@ -308,3 +308,40 @@ def test_the_divisor_holds_the_same_rounded_probabilities_as_the_sums(kb, vb, G,
             bound = np.abs(o) * (2.0 ** -11 + 2.0 ** -20) + 3.5 * (1 << (vb - 1)) * 2.0 ** -11 + 2 * eps_s * spread
             err = np.abs(out[b, j].double().cpu().numpy() - o)
             assert (err <= bound).all(), (b, j, float((err / bound).max()))
+
+
+# ------------------------------------------------------------- one long request among short ones
+@pytest.mark.parametrize("G,dtype", [(4, "bf16"), (8, "f16"), (16, "f32")])
+def test_decode_of_one_long_request_among_short_ones(G, dtype):
+    # nearly all ranges belong to one request: its rows join hundreds of partials, the others' one or two
+    lens = [200] * 30 + [40000] + [1, 0, 65] * 11
+    pool = Pool(17, 400, 1, 256, 4, 4, 0)
+    _, check = decode_case(pool, G, dtype, lens, seed=5)
+    for b in (0, 29, 30, 31, 33, len(lens) - 1):
+        for j in {0, G - 1}:
+            check(b, j)
+
+
+def test_captured_decodes_without_a_workspace_on_a_given_stream():
+    # two graphs, each with the workspace and the output of its own memory, replayed in turn and beside eager calls
+    pool = Pool(23, 40, 2, 64, 4, 4, 0)
+    table, lens = i32(np.random.RandomState(2).permutation(40).reshape(4, 10)), i32([640, 33, 200, 64])
+    qs = [torch.randn(4, 8, D, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    refs = [pool.cache.decode(q, table, lens, 640) for q in qs]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for q in qs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(pool.cache.decode(q, table, lens, 640, stream=side))
+        graphs.append(g)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+        eager = pool.cache.decode(qs[0], table, lens, 640)
+        torch.cuda.synchronize()
+        assert torch.equal(eager, refs[0]) and all(torch.equal(o, r) for o, r in zip(outs, refs))
+    del graphs
